@@ -1,0 +1,770 @@
+"""What is measured of the fine-tuning operators: the losses that make a step's
+gradients and the many-tensor AdamW step that consumes them.
+
+Each case names one pass through an operator; `run` computes it either in its
+plain form (elementary torch operations, `own = False`) or through the
+package's entry points (`own = True`), on the same inputs:
+
+  logp    log-probabilities of the labels from the logits (forward alone: the
+          pass of a frozen reference model)
+  pref    preference loss of pairs of sequences, from the logits to their
+          gradient
+  policy  clipped policy loss with a KL term, from the logits to their gradient
+  norm    sum of squares and inf/NaN test over all gradients of a model
+  adam    one AdamW step over all tensors of a model, states in 32 or 8 bits,
+          clipped by the global norm
+"""
+import math
+
+import numpy as np
+import torch
+
+own = False
+
+DEV = "cuda:0"
+_DT = {"f16": torch.float16, "bf16": torch.bfloat16, "f32": torch.float32}
+_BLOCK = 256  # elements that share one scale of the 8-bit states
+
+
+# ------------------------------------------------------------------- cases
+def listed():
+    return [
+        # scoring a handful of short genomic sequences: 4096-word vocabulary, latency counts
+        dict(name="logp_small", op="logp", rows=96, vocab=4096, pad=0, dtype="f16", temp=1.0),
+        # a reference model's scores of 4096 tokens, 128256-word vocabulary
+        dict(name="logp_large", op="logp", rows=4096, vocab=128256, pad=0, dtype="bf16",
+             temp=1.0),
+        # two short pairs on a 50257-word vocabulary: odd rows, no row but every eighth aligned
+        dict(name="pref_small", op="pref", pairs=2, longest=24, vocab=50257, pad=0, dtype="bf16",
+             kind="sigmoid", scale=1.0),
+        # fp32 logits, length-averaged squared form
+        dict(name="pref_f32", op="pref", pairs=4, longest=160, vocab=50257, pad=47, dtype="f32",
+             kind="squared", scale=1.0),
+        # a usual micro-batch of pairs on a 32000-word vocabulary
+        dict(name="pref_mid", op="pref", pairs=16, longest=512, vocab=32000, pad=0, dtype="bf16",
+             kind="sigmoid", scale=1.0),
+        # a few sampled tokens, fp16 with a loss scale
+        dict(name="policy_small", op="policy", rows=61, vocab=50257, pad=0, dtype="f16",
+             kl=0.05, temp=1.0, scale=65536.0),
+        # a rollout micro-batch of 4096 tokens on a 128256-word vocabulary, sampled at 0.8
+        dict(name="policy_large", op="policy", rows=4096, vocab=128256, pad=0, dtype="bf16",
+             kl=0.05, temp=0.8, scale=1.0),
+        # three tensors, 10272 elements: the smallest call
+        dict(name="norm_tiny", op="norm", model="tiny", dtype="f16", packed=False, scale=1024.0),
+        # two layers of width 4096: 436 million gradients
+        dict(name="norm_large", op="norm", model="layers4096", dtype="bf16", packed=False,
+             scale=1.0),
+        # 2000 small tensors of 64 to 6144 elements, fp16 gradients, fp32 states
+        dict(name="adam32_small", op="adam", model="small2000", dtype="f16", param="f16", bits=32,
+             packed=False, scale=65536.0, step=3, adamw=True, clip=1.0),
+        # a 124-million-parameter model of 148 tensors, states in 8 bits
+        dict(name="adam8_mid", op="adam", model="width768", dtype="bf16", param="bf16", bits=8,
+             packed=False, scale=1.0, step=11, adamw=True, clip=1.0),
+        # two layers of width 4096, states in 8 bits
+        dict(name="adam8_large", op="adam", model="layers4096", dtype="bf16", param="bf16",
+             bits=8, packed=False, scale=1.0, step=200, adamw=True, clip=1.0),
+    ]
+
+
+def _log_int(rng, lo, hi):
+    return int(round(math.exp(rng.uniform(math.log(lo), math.log(hi)))))
+
+
+def draw(rng):
+    op = rng.choice(["logp", "pref", "policy", "norm", "adam"])
+    if op in ("logp", "pref", "policy"):
+        dtype = rng.choice(["bf16", "bf16", "f16", "f32"])
+        vocab = _log_int(rng, 1000, 131072)
+        pad = rng.choice([0, 0, rng.randrange(1, 64), (-vocab) % 64])
+        most = 4096 * 128256 // (vocab + pad) // (2 if dtype == "f32" else 1)
+        if op == "pref":
+            longest = _log_int(rng, 2, 1024)
+            pairs = _log_int(rng, 1, 64)
+            pairs = max(1, min(pairs, most // 2 // (2 * longest)))
+            return dict(op=op, pairs=pairs, longest=min(longest, max(1, most // 4)), vocab=vocab,
+                        pad=pad, dtype=dtype, kind=rng.choice(["sigmoid", "squared"]),
+                        scale=1.0 if dtype != "f16" else 4096.0)
+        rows = min(_log_int(rng, 1, 16384), most)
+        case = dict(op=op, rows=rows, vocab=vocab, pad=pad, dtype=dtype,
+                    temp=rng.choice([1.0, 0.7, 1.25]))
+        if op == "policy":
+            case.update(kl=rng.choice([0.0, 0.02, 0.1]), scale=1.0 if dtype != "f16" else 16384.0)
+        return case
+    n = _log_int(rng, 1, 800)
+    model = "drawn:%d:%d:%d" % (n, _log_int(rng, 300, min(1 << 24, (1 << 28) // n)),
+                                rng.randrange(1 << 30))
+    dtype = rng.choice(["bf16", "f16", "f32"])
+    case = dict(op=op, model=model, dtype=dtype, packed=rng.random() < 0.3,
+                scale=1.0 if dtype != "f16" else 8192.0)
+    if op == "adam":
+        case.update(param=rng.choice(["bf16", "f16", "none"]), bits=rng.choice([8, 8, 32]),
+                    step=_log_int(rng, 1, 5000), adamw=rng.random() < 0.8,
+                    clip=rng.choice([0.0, 1.0]))
+    return case
+
+
+# ------------------------------------------------------------- model shapes
+def _shapes(model):
+    """Element counts of a model's tensors, and which of them decay (matrices)."""
+    if model == "tiny":
+        return [2048, 32, 8192], [1, 0, 1]
+    if model == "layers4096":  # two layers of width 4096, 1024 kv, 14336 inner
+        d, kv, ffn = 4096, 1024, 14336
+        layer = [(d, 0), (d * d, 1), (kv * d, 1), (kv * d, 1), (d * d, 1), (d, 0), (ffn * d, 1),
+                 (ffn * d, 1), (d * ffn, 1)]
+        both = layer * 2 + [(d, 0)]
+    elif model == "width768":  # 12 layers of width 768, vocabulary 50257, 1024 positions
+        d, f = 768, 4 * 768
+        layer = [(d, 0), (d, 0), (3 * d * d, 1), (3 * d, 0), (d * d, 1), (d, 0), (d, 0), (d, 0),
+                 (d * f, 1), (f, 0), (f * d, 1), (d, 0)]
+        both = [(50257 * d, 1), (1024 * d, 1)] + layer * 12 + [(d, 0), (d, 0)]
+    elif model == "small2000":
+        r = np.random.default_rng(5)
+        both = [(int(s), 0) for s in r.integers(64, 6145, 2000)]
+    else:  # "drawn:count:largest:seed", sizes over their logarithm
+        _, n, largest, seed = model.split(":")
+        r = np.random.default_rng(int(seed))
+        sizes = np.exp(r.uniform(0.0, math.log(int(largest)), int(n))).astype(np.int64)
+        sizes[r.integers(0, int(n))] = int(largest)
+        both = [(int(max(s, 1)), int(s > 4096)) for s in sizes]
+    return [s for s, _ in both], [g for _, g in both]
+
+
+def _offsets(sizes, packed):
+    """Where each tensor starts in the buffer that holds them all: tightly packed, or each
+    at a multiple of 256 elements."""
+    at, out = 0, []
+    for s in sizes:
+        out.append(at)
+        at += s if packed else -(-s // _BLOCK) * _BLOCK
+    return out, at
+
+
+def _padded_offsets(sizes):
+    return _offsets(sizes, False)
+
+
+# ------------------------------------------------------------------- inputs
+def _logits(case, rows, g):
+    v, st, dt = case["vocab"], case["vocab"] + case["pad"], _DT[case["dtype"]]
+    buf = torch.empty(rows, st, device=DEV, dtype=dt)
+    labels = torch.randint(0, v, (rows,), generator=g, device=DEV)
+    labels[torch.rand(rows, generator=g, device=DEV) < 0.2] = -100  # prompt tokens
+    step = max(1, (1 << 26) // st)
+    logp = torch.zeros(rows, device=DEV)
+    temp = case.get("temp", 1.0)
+    for a in range(0, rows, step):
+        x = torch.randn(min(step, rows - a), st, generator=g, device=DEV) * 2.5
+        lab = labels[a:a + step].clamp(min=0)
+        x.scatter_add_(1, lab[:, None], torch.rand(x.shape[0], 1, generator=g, device=DEV) * 12.0)
+        buf[a:a + step] = x.to(dt)
+        y = buf[a:a + step, :v].float() / temp
+        logp[a:a + step] = y.gather(1, lab[:, None])[:, 0] - torch.logsumexp(y, 1)
+    return buf[:, :v], labels, logp
+
+
+def _seq_offsets(case):
+    r = np.random.default_rng(1000 * case["pairs"] + case["longest"])
+    lens = r.integers(0 if case["longest"] > 4 else 1, case["longest"] + 1, 2 * case["pairs"])
+    lens[0] = case["longest"]
+    return np.concatenate([[0], np.cumsum(lens)]).astype(np.int64)
+
+
+def _scalars(case, step, coef):
+    """The update's fp32 scalars, formed in double and rounded once, for the two groups of
+    tensors (without and with weight decay)."""
+    lr, b1, b2, eps = 1e-3, 0.9, 0.999, 1e-8
+    f = lambda x: float(np.float32(x))
+    out = []
+    for wd in (0.0, 0.01):
+        out.append(dict(inv=f(coef / case["scale"]), b1=f(b1), omb1=f(1 - b1), b2=f(b2),
+                        omb2=f(1 - b2), step=f(lr / (1 - b1 ** step)),
+                        rsbc2=f(1 / math.sqrt(1 - b2 ** step)), eps=f(eps),
+                        decay=f(1 - lr * wd) if case["adamw"] else 1.0, wd=f(wd)))
+    return out
+
+
+def prepare(case, seed):
+    g = torch.Generator(device=DEV)
+    g.manual_seed(seed)
+    op = case["op"]
+    s = dict(case=case, op=op)
+    if op in ("logp", "pref", "policy"):
+        if op == "pref":
+            cu = _seq_offsets(case)
+            s["cu"] = torch.from_numpy(cu).to(DEV)
+            rows = int(cu[-1])
+        else:
+            rows = case["rows"]
+        s["logits"], s["labels"], logp = _logits(case, rows, g)
+        if op == "pref":
+            s["ref"] = logp + torch.randn(rows, generator=g, device=DEV) * 0.2
+        if op == "policy":
+            s["old"] = logp + torch.randn(rows, generator=g, device=DEV) * 0.15
+            s["ref"] = logp + torch.randn(rows, generator=g, device=DEV) * 0.3
+            s["adv"] = torch.randn(rows, generator=g, device=DEV)
+            # tokens of one answer share 1 / its length
+            s["weight"] = 1.0 / torch.randint(1, 400, (rows,), generator=g, device=DEV).float()
+        if own:
+            f = lambda *n: torch.empty(*n, device=DEV)
+            s.update(logp=f(rows), lse=f(rows))
+            if op != "logp":
+                s["dlogits"] = torch.empty_strided(s["logits"].shape, s["logits"].stride(),
+                                                   device=DEV, dtype=s["logits"].dtype)
+            if op == "pref":
+                s.update(dlogp=f(rows), loss=f(1), pair_loss=f(case["pairs"]),
+                         rewards=f(case["pairs"], 2))
+            if op == "policy":
+                s.update(terms=f(rows, 4), loss=f(4))
+        return s
+    sizes, decay = _shapes(case["model"])
+    offs, total = _offsets(sizes, case["packed"])
+    _, padded = _padded_offsets(sizes)
+    dt = _DT[case["dtype"]]
+    real = None
+    if not case["packed"]:
+        real = torch.zeros(total, dtype=torch.bool, device=DEV)
+        for o, n in zip(offs, sizes):
+            real[o:o + n] = True
+
+    def noise(sigma, dtype):
+        out = torch.empty(total, dtype=dtype, device=DEV)
+        for a in range(0, total, 1 << 26):
+            x = torch.randn(min(1 << 26, total - a), generator=g, device=DEV) * sigma
+            # one gradient in a hundred is much larger
+            x = torch.where(torch.rand(x.numel(), generator=g, device=DEV) < 0.01, x * 30.0, x)
+            out[a:a + (1 << 26)] = x.to(dtype)
+        return out if real is None else out.masked_fill_(~real, 0)
+
+    s.update(sizes=sizes, decay=decay, offs=offs, total=total)
+    s["grad"] = noise(1e-4 * case["scale"], dt)
+    if op == "norm":
+        if own:
+            _bind(s)
+            s["sumsq"] = torch.empty(1, dtype=torch.float64, device=DEV)
+            s["flag"] = torch.empty(1, dtype=torch.int32, device=DEV)
+        return s
+    s["t"] = case["step"] - 1
+    s["seed"] = seed & 0x7FFFFFFF
+    s["master"] = noise(0.02, torch.float32)
+    if case["param"] != "none":
+        s["param"] = s["master"].to(_DT[case["param"]])
+    s["sumsq"] = s["grad"].double().square().sum().reshape(1)
+    s["flag"] = torch.zeros(1, dtype=torch.int32, device=DEV)
+    if case["bits"] == 32:
+        s["m"] = noise(2e-5, torch.float32)
+        s["v"] = noise(5e-5, torch.float32).square_()
+    else:
+        nb = padded // _BLOCK
+        s["m8"] = (torch.randn(padded, generator=g, device=DEV) * 60).clamp_(-240, 240).to(
+            torch.float8_e4m3fn).view(torch.uint8)
+        s["v8"] = torch.randint(120, 250, (padded,), generator=g, device=DEV, dtype=torch.uint8)
+        s["m_scale"] = torch.randint(108, 113, (nb,), generator=g, device=DEV, dtype=torch.uint8)
+        s["v_scale"] = torch.randint(92, 98, (nb,), generator=g, device=DEV, dtype=torch.uint8)
+        if case["step"] == 1:  # the first step starts from nothing
+            for k in ("m8", "v8", "m_scale", "v_scale"):
+                s[k].zero_()
+        for o, n in zip(_padded_offsets(sizes)[0], sizes):  # nothing behind a tensor's end
+            end = o + -(-n // _BLOCK) * _BLOCK
+            s["m8"][o + n:end] = 0
+            s["v8"][o + n:end] = 0
+    if own:
+        _bind(s)
+        if case["bits"] == 8:
+            s["m"] = torch.empty(padded, device=DEV)
+            s["v"] = torch.empty(padded, device=DEV)
+    return s
+
+
+def _views(flat, offs, sizes):
+    return [flat[o:o + n] for o, n in zip(offs, sizes)]
+
+
+def _bind(s):
+    """The tensors of a model, handed to the package once."""
+    import zero_partitioned_mixed_plan_amd as z
+    case, sizes = s["case"], s["sizes"]
+    bits = case.get("bits", 32)
+    many = z.zero_many_create(sizes, state_bits=bits, groups=s["decay"], n_groups=2)
+    kw = dict(grads=_views(s["grad"], s["offs"], sizes))
+    if s["op"] == "adam":
+        kw["master"] = _views(s["master"], s["offs"], sizes)
+        if "param" in s:
+            kw["param"] = _views(s["param"], s["offs"], sizes)
+        if bits == 32:
+            kw["exp_avg"] = _views(s["m"], s["offs"], sizes)
+            kw["exp_avg_sq"] = _views(s["v"], s["offs"], sizes)
+        else:
+            po, _ = _padded_offsets(sizes)
+            bo = [o // _BLOCK for o in po]
+            bn = [-(-n // _BLOCK) for n in sizes]
+            kw["exp_avg"] = _views(s["m8"], po, sizes)
+            kw["exp_avg_sq"] = _views(s["v8"], po, sizes)
+            kw["exp_avg_scale"] = _views(s["m_scale"], bo, bn)
+            kw["exp_avg_sq_scale"] = _views(s["v_scale"], bo, bn)
+        s["hparams"] = [z.AdamHParams(weight_decay=wd, adamw=case["adamw"]) for wd in (0.0, 0.01)]
+    z.zero_many_bind(many, **kw)
+    if s["op"] == "adam":
+        z.zero_many_state_upload(many, s["t"], z.LossScaler(case["scale"], dynamic=False),
+                                 seed=s["seed"])
+    s["many"] = many
+
+
+# ------------------------------------------------------------ one pass
+def run(state):
+    return _run_own(state) if own else _run_plain(state)
+
+
+def _run_own(s):
+    import zero_partitioned_mixed_plan_amd as z
+    case, op = s["case"], s["op"]
+    if op == "logp":
+        z.zero_token_logp(s["logits"], s["labels"], s["logp"], s["lse"],
+                          inv_temperature=1.0 / case["temp"])
+        return {"logp": s["logp"], "lse": s["lse"]}
+    if op == "pref":
+        z.zero_token_logp(s["logits"], s["labels"], s["logp"], s["lse"])
+        z.zero_preference_loss(s["logp"], s["ref"], s["cu"], s["loss"], s["pair_loss"],
+                               s["rewards"], s["dlogp"], labels=s["labels"], kind=case["kind"],
+                               beta=0.1, label_smoothing=0.05 if case["kind"] == "sigmoid" else 0,
+                               average=case["kind"] == "squared", norm=1.0 / case["pairs"],
+                               loss_scale=case["scale"])
+        z.zero_token_logp_grad(s["logits"], s["labels"], s["lse"], s["dlogp"], s["dlogits"])
+        return {k: s[k] for k in ("loss", "pair_loss", "rewards", "logp", "dlogits")}
+    if op == "policy":
+        z.zero_policy_loss(s["logits"], s["labels"], s["old"], s["adv"], s["dlogits"], s["logp"],
+                           s["terms"], s["loss"], ref_logp=s["ref"], weight=s["weight"],
+                           clip_low=0.2, clip_high=0.28, kl_coef=case["kl"],
+                           norm=1.0 / case["rows"], inv_temperature=1.0 / case["temp"],
+                           loss_scale=case["scale"])
+        return {k: s[k] for k in ("loss", "logp", "dlogits")}
+    if op == "norm":
+        z.zero_many_grad_norm(s["many"], s["sumsq"], s["flag"])
+        return {"sumsq": s["sumsq"], "flag": s["flag"]}
+    z.zero_many_adam_step(s["many"], s["hparams"], flag=s["flag"],
+                          sumsq=s["sumsq"] if case["clip"] else None, max_norm=case["clip"])
+    if case["bits"] == 8:
+        z.zero_many_state_values(s["many"], s["m"], s["v"])
+    return {k: s[k] for k in ("master", "param", "m", "v") if k in s}
+
+
+def _plain_lse(x):
+    m = x.max(1, keepdim=True).values
+    return (m[:, 0].double() + (x - m).exp().sum(1, dtype=torch.float64).log())
+
+
+def _plain_logp(s, temp):
+    """Rows in pieces: x and log-sum-exp of each, in fp32 with 64-bit sums."""
+    logits, labels = s["logits"], s["labels"]
+    logp = torch.zeros(labels.numel(), dtype=torch.float64, device=DEV)
+    lse = torch.zeros_like(logp)
+    step = max(1, (1 << 27) // logits.shape[1])
+    for a in range(0, labels.numel(), step):
+        x = logits[a:a + step].float() * float(np.float32(1.0 / temp))
+        lse[a:a + step] = _plain_lse(x)
+        at = x.gather(1, labels[a:a + step].clamp(min=0)[:, None])[:, 0]
+        logp[a:a + step] = at.double() - lse[a:a + step]
+    live = labels >= 0
+    return torch.where(live, logp, 0.0), torch.where(live, lse, 0.0)
+
+
+def _plain_dlogits(s, temp, lse, dlogp):
+    logits, labels = s["logits"], s["labels"]
+    out = torch.empty_strided(logits.shape, logits.stride(), device=DEV, dtype=logits.dtype)
+    step = max(1, (1 << 27) // logits.shape[1])
+    inv = float(np.float32(1.0 / temp))
+    for a in range(0, labels.numel(), step):
+        lab = labels[a:a + step]
+        x = logits[a:a + step].float() * inv
+        d = -(x - lse[a:a + step, None].float()).exp()
+        d.scatter_add_(1, lab.clamp(min=0)[:, None], torch.ones_like(d[:, :1]))
+        d *= (dlogp[a:a + step] * inv)[:, None]
+        out[a:a + step] = torch.where((lab >= 0)[:, None], d, 0.0).to(out.dtype)
+    return out
+
+
+def _plain_pref(case, logp, ref, labels, cu):
+    """Loss, per-pair loss, rewards and the gradient per token, in the type of logp."""
+    n, b = logp.numel(), 2 * case["pairs"]
+    live = (labels >= 0).to(logp.dtype)
+    diff = (logp - ref.to(logp.dtype)) * live
+    seq = torch.searchsorted(cu, torch.arange(n, device=DEV), right=True) - 1
+    total = torch.zeros(b, dtype=logp.dtype, device=DEV).index_add_(0, seq, diff)
+    count = torch.zeros(b, dtype=logp.dtype, device=DEV).index_add_(0, seq, live)
+    share = torch.ones_like(count)
+    beta = float(np.float32(0.1))
+    if case["kind"] == "squared":
+        share = 1.0 / count.clamp(min=1.0)
+    d = (total * share).view(-1, 2)
+    delta = d[:, 0] - d[:, 1]
+    if case["kind"] == "squared":
+        e = delta - 1.0 / (2.0 * beta)
+        pair, dd = e * e, 2.0 * e
+    else:
+        h, eps = beta * delta, float(np.float32(0.05))
+        sp = lambda y: y.clamp(min=0.0) + (1.0 + (-y.abs()).exp()).log()
+        pair = (1.0 - eps) * sp(-h) + eps * sp(h)
+        dd = beta * (eps / (1.0 + (-h).exp()) - (1.0 - eps) / (1.0 + h.exp()))
+    k = case["scale"] / case["pairs"]
+    per_seq = torch.stack([dd, -dd], 1).reshape(-1) * share * k
+    return pair.mean().reshape(1), pair, beta * d, per_seq[seq] * live
+
+
+def _plain_policy(case, s, logp):
+    """Loss terms and the gradient per token, in the type of logp."""
+    t = lambda k: s[k].to(logp.dtype)
+    live = (s["labels"] >= 0).to(logp.dtype)
+    a, w = t("adv"), t("weight") * live
+    ratio = (logp - t("old")).exp()
+    kept, cut = ratio * a, ratio.clamp(1.0 - float(np.float32(0.2)), 1.0 + float(np.float32(0.28))) * a
+    pg = -torch.minimum(kept, cut)
+    q = t("ref") - logp
+    kl = q.exp() - q - 1.0
+    kc, norm = float(np.float32(case["kl"])), 1.0 / case["rows"]
+    d = torch.where(kept <= cut, -a * ratio, 0.0) + kc * (1.0 - q.exp())
+    part = lambda y: norm * (w * torch.where(live > 0, y, 0.0)).sum()
+    loss = torch.stack([part(pg) + kc * part(kl), part(pg), part(kl),
+                        part((kept > cut).to(logp.dtype))])
+    return loss, torch.where(live > 0, d, 0.0) * w * (case["scale"] * norm)
+
+
+def _run_plain(s):
+    case, op = s["case"], s["op"]
+    f32 = torch.float32
+    if op == "logp":
+        logp, lse = _plain_logp(s, case["temp"])
+        return {"logp": logp.to(f32), "lse": lse.to(f32)}
+    if op == "pref":
+        logp, lse = _plain_logp(s, 1.0)
+        loss, pair, rewards, dlogp = _plain_pref(case, logp, s["ref"], s["labels"], s["cu"])
+        return {"loss": loss.to(f32), "pair_loss": pair.to(f32), "rewards": rewards.to(f32),
+                "logp": logp.to(f32), "dlogits": _plain_dlogits(s, 1.0, lse, dlogp.to(f32))}
+    if op == "policy":
+        logp, lse = _plain_logp(s, case["temp"])
+        loss, dlogp = _plain_policy(case, s, logp)
+        return {"loss": loss.to(f32), "logp": logp.to(f32),
+                "dlogits": _plain_dlogits(s, case["temp"], lse, dlogp.to(f32))}
+    if op == "norm":
+        total = torch.zeros(1, dtype=torch.float64, device=DEV)
+        bad = torch.zeros(1, dtype=torch.int32, device=DEV)
+        for a in range(0, s["total"], 1 << 27):
+            g = s["grad"][a:a + (1 << 27)]
+            total += g.double().square().sum()
+            bad |= (~torch.isfinite(g)).any().int()
+        return {"sumsq": total, "flag": bad}
+    return _plain_adam(s)
+
+
+# --------------------------------------------------------- the AdamW step
+def _to_blocks(flat, s):
+    """Tensors of the buffer, each from a block's start, padded with zeros: [blocks, 256]."""
+    offs, total = _padded_offsets(s["sizes"])
+    if not s["case"]["packed"]:
+        return flat.view(-1, _BLOCK)
+    out = torch.zeros(total, dtype=flat.dtype, device=DEV)
+    for o, p, n in zip(s["offs"], offs, s["sizes"]):
+        out[p:p + n] = flat[o:o + n]
+    return out.view(-1, _BLOCK)
+
+
+def _from_blocks(blocks, s, flat):
+    offs, _ = _padded_offsets(s["sizes"])
+    if not s["case"]["packed"]:
+        return
+    b = blocks.reshape(-1)
+    for o, p, n in zip(s["offs"], offs, s["sizes"]):
+        flat[o:o + n] = b[p:p + n]
+
+
+def _per_block(s, key, sc, dtype=torch.float32):
+    """A scalar of each tensor's group, one per block."""
+    n = torch.tensor([-(-k // _BLOCK) for k in s["sizes"]])
+    v = torch.tensor([sc[0][key], sc[1][key]], dtype=torch.float64)[torch.tensor(s["decay"])]
+    return torch.repeat_interleave(v, n).to(DEV).to(dtype)[:, None]
+
+
+def _key(seed, t):
+    m = (1 << 64) - 1
+    z = (seed + t * 0x9E3779B97F4A7C15) & m
+    z = ((z ^ (z >> 30)) * 0xBF58476D1CE4E5B9) & m
+    z = ((z ^ (z >> 27)) * 0x94D049BB133111EB) & m
+    return (z ^ (z >> 31)) & 0xFFFFFFFF
+
+
+def _random16(first, count, key):
+    """16 random bits for elements first .. first + count - 1."""
+    low = 0xFFFFFFFF
+    pair = torch.arange(first // 2, (first + count) // 2, device=DEV)
+    x = ((pair & low) * 0x9E3779B1 + ((key ^ (((pair >> 32) * 0x6A09E667) & low)))) & low
+    x ^= x >> 16
+    x = (x * 0xBB67AE85) & low
+    x ^= x >> 15
+    return torch.stack([x & 0xFFFF, x >> 16], 1).reshape(-1, _BLOCK).int()
+
+
+def _ldexp(x, e):
+    """x 2^e, rounded once to fp32 (e: one per block; both powers are normal in 64 bits)."""
+    return (x.double() * torch.exp2(e.double())).float()
+
+
+def _unpack8(s, lo, hi):
+    em = s["m_scale"][lo:hi].int()[:, None]
+    ev = s["v_scale"][lo:hi].int()[:, None]
+    m = s["m8"].view(-1, _BLOCK)[lo:hi].view(torch.float8_e4m3fn).float()
+    v = (s["v8"].view(-1, _BLOCK)[lo:hi].int() << 20).view(torch.float32)
+    return _ldexp(m, em - 134), _ldexp(v, ev - 31)
+
+
+def _exponent(x):
+    return (x.abs().amax(1, keepdim=True).view(torch.int32) >> 23)
+
+
+def _pack8(s, lo, hi, m, v, r):
+    em, ev = _exponent(m), _exponent(v)
+    s["m_scale"][lo:hi] = em[:, 0].to(torch.uint8)
+    s["v_scale"][lo:hi] = ev[:, 0].to(torch.uint8)
+    s["m8"].view(-1, _BLOCK)[lo:hi] = _ldexp(m, 134 - em).to(torch.float8_e4m3fn).view(torch.uint8)
+    code = ((_ldexp(v, 31 - ev).view(torch.int32) + (r << 4)) >> 20).clamp(max=255)
+    s["v8"].view(-1, _BLOCK)[lo:hi] = torch.where(v > 0, code.clamp(min=1), 0).to(torch.uint8)
+
+
+def _clip_coef(case, sumsq):
+    if not case["clip"]:
+        return 1.0
+    return min(1.0, case["clip"] / (math.sqrt(float(sumsq)) / case["scale"] + 1e-6))
+
+
+def _plain_adam(s):
+    """Every operation rounded once to fp32, in the order of the flat shard's update.  The
+    clip is a device value, so it is one here too."""
+    case = s["case"]
+    s["t"] += 1
+    sc = _scalars(case, s["t"], 1.0)
+    if case["clip"]:
+        coef = (case["clip"] / (s["sumsq"].sqrt() / case["scale"] + 1e-6)).clamp(max=1.0)
+    else:
+        coef = torch.ones(1, dtype=torch.float64, device=DEV)
+    inv = (coef / case["scale"]).float()
+    decay, wd = _per_block(s, "decay", sc), _per_block(s, "wd", sc)
+    c = sc[0]
+    key = _key(s["seed"], s["t"])
+    grad, master = _to_blocks(s["grad"], s), _to_blocks(s["master"], s)
+    eight = case["bits"] == 8
+    if not eight:
+        mb, vb = _to_blocks(s["m"], s), _to_blocks(s["v"], s)
+    nb = grad.shape[0]
+    if eight:
+        m_out, v_out = (torch.empty(nb, _BLOCK, device=DEV) for _ in range(2))
+    param = _to_blocks(s["param"], s) if "param" in s else None
+    step = 1 << 17  # blocks in a piece
+    for lo in range(0, nb, step):
+        hi = min(nb, lo + step)
+        p = master[lo:hi]
+        g = grad[lo:hi].float() * inv
+        if not case["adamw"]:
+            g = g + wd[lo:hi] * p
+        m, v = _unpack8(s, lo, hi) if eight else (mb[lo:hi], vb[lo:hi])
+        m = c["b1"] * m + c["omb1"] * g
+        v = c["b2"] * v + c["omb2"] * (g * g)
+        d = v.double().sqrt().float() * c["rsbc2"] + c["eps"]
+        u = (m.double() / d.double()).float()
+        master[lo:hi] = p * decay[lo:hi] - c["step"] * u
+        if eight:
+            _pack8(s, lo, hi, m, v, _random16(lo * _BLOCK, (hi - lo) * _BLOCK, key))
+            m_out[lo:hi], v_out[lo:hi] = _unpack8(s, lo, hi)
+        else:
+            mb[lo:hi], vb[lo:hi] = m, v
+        if param is not None:
+            param[lo:hi] = master[lo:hi].to(param.dtype)
+    _from_blocks(master, s, s["master"])
+    out = {"master": s["master"]}
+    if param is not None:
+        _from_blocks(param, s, s["param"])
+        out["param"] = s["param"]
+    if eight:
+        out["m"], out["v"] = m_out.view(-1), v_out.view(-1)
+    else:
+        _from_blocks(mb, s, s["m"])
+        _from_blocks(vb, s, s["v"])
+        out["m"], out["v"] = s["m"], s["v"]
+    return out
+
+
+# ------------------------------------------------------------------- work
+def work(case):
+    op = case["op"]
+    if op in ("logp", "pref", "policy"):
+        rows = case["rows"] if op != "pref" else int(_seq_offsets(case)[-1])
+        one = rows * case["vocab"]
+        size = torch.empty(0, dtype=_DT[case["dtype"]]).element_size()
+        if op == "logp":
+            return {"bytes": one * size + rows * 16, "flops": 5 * one}
+        return {"bytes": 2 * one * size + rows * 40, "flops": 9 * one}
+    sizes, _ = _shapes(case["model"])
+    n = sum(sizes)
+    gb = torch.empty(0, dtype=_DT[case["dtype"]]).element_size()
+    if op == "norm":
+        return {"bytes": n * gb, "flops": 2 * n}
+    per = gb + 8 + (2 if case["param"] != "none" else 0)
+    per += 16 if case["bits"] == 32 else 4 + 8  # 8 bits: the codes, and the values they stand for
+    return {"bytes": n * per, "flops": 16 * n}
+
+
+# ------------------------------------------------------------------ exact
+def exact(case, seed):
+    global own
+    before, own = own, False
+    try:
+        s = prepare(case, seed)
+    finally:
+        own = before
+    op = case["op"]
+    if op in ("logp", "pref", "policy"):
+        return _exact_loss(case, s)
+    if op == "norm":
+        total = np.float64(0.0)
+        parts = [float((s["grad"][a:a + (1 << 24)].double() ** 2).sum())
+                 for a in range(0, s["total"], 1 << 24)]
+        total = math.fsum(parts)
+        return {"sumsq": torch.tensor([total], dtype=torch.float64, device=DEV),
+                "flag": torch.isnan(s["grad"].double().sum()).int().reshape(1)}
+    return _exact_adam(case, s)
+
+
+def _exact_loss(case, s):
+    """Row by row from the definitions, in 64 bits."""
+    x, lab = s["logits"], s["labels"]
+    rows, v = x.shape
+    inv = float(np.float32(1.0 / case.get("temp", 1.0)))
+    keep = lab >= 0
+    lse = torch.empty(rows, dtype=torch.float64, device=DEV)
+    logp = torch.empty_like(lse)
+    step = max(1, (1 << 26) // v)
+    for a in range(0, rows, step):
+        y = x[a:a + step].double() * inv
+        lse[a:a + step] = torch.logsumexp(y, 1)
+        at = lab[a:a + step].clamp(min=0)
+        logp[a:a + step] = y[torch.arange(y.shape[0], device=DEV), at] - lse[a:a + step]
+    logp[~keep] = 0
+    lse[~keep] = 0
+    if case["op"] == "logp":
+        return {"logp": logp, "lse": lse}
+    out = {"logp": logp}
+    d = torch.zeros_like(logp)
+    if case["op"] == "pref":
+        cu = s["cu"].cpu().tolist()
+        diff = torch.where(keep, logp - s["ref"].double(), 0.0).cpu().numpy()
+        live = keep.cpu().numpy()
+        grad = np.zeros(rows)
+        beta, pair_loss, rewards = float(np.float32(0.1)), [], []
+        for i in range(case["pairs"]):
+            mean, cnt = [], []
+            for j in (0, 1):
+                a, b = cu[2 * i + j], cu[2 * i + j + 1]
+                n = int(live[a:b].sum())
+                cnt.append(max(n, 1) if case["kind"] == "squared" else 1)
+                mean.append(math.fsum(diff[a:b]) / cnt[-1])
+            delta = mean[0] - mean[1]
+            if case["kind"] == "squared":
+                pair_loss.append((delta - 0.5 / beta) ** 2)
+                slope = 2 * (delta - 0.5 / beta)
+            else:
+                e, h = float(np.float32(0.05)), beta * delta
+                pair_loss.append((1 - e) * np.logaddexp(0, -h) + e * np.logaddexp(0, h))
+                slope = beta * (1 / (1 + math.exp(-h)) - (1 - e))
+            rewards.append([beta * mean[0], beta * mean[1]])
+            for j, sign in ((0, 1.0), (1, -1.0)):
+                a, b = cu[2 * i + j], cu[2 * i + j + 1]
+                grad[a:b] = sign * slope / cnt[j] * case["scale"] / case["pairs"] * live[a:b]
+        f = lambda y: torch.tensor(np.array(y), dtype=torch.float64, device=DEV)
+        out.update(loss=f([np.mean(pair_loss)]), pair_loss=f(pair_loss), rewards=f(rewards))
+        d = f(grad)
+    else:
+        lo, hi = 1 - float(np.float32(0.2)), 1 + float(np.float32(0.28))
+        kc = float(np.float32(case["kl"]))
+        lp, old, ref, adv, w = (t[keep].double() for t in (logp, s["old"], s["ref"], s["adv"],
+                                                           s["weight"]))
+        r = torch.exp(lp - old)
+        capped = torch.where(adv >= 0, r > hi, r < lo)  # where the clip holds the gain down
+        obj = torch.where(capped, torch.where(adv >= 0, hi, lo), r) * adv
+        back = torch.exp(ref - lp)
+        kl = torch.expm1(ref - lp) - (ref - lp)
+        n = case["rows"]
+        parts = [float((w * y).sum()) / n for y in (-obj, kl, capped.double())]
+        out["loss"] = torch.tensor([parts[0] + kc * parts[1], *parts], dtype=torch.float64,
+                                   device=DEV)
+        d[keep] = (kc * (1 - back) - torch.where(capped, 0.0, r * adv)) * w * case["scale"] / n
+    grad = torch.empty(rows, v, dtype=torch.float64, device=DEV)
+    for a in range(0, rows, step):
+        p = torch.exp(x[a:a + step].double() * inv - lse[a:a + step, None])
+        p = -p
+        i = torch.arange(p.shape[0], device=DEV)
+        p[i, lab[a:a + step].clamp(min=0)] += 1
+        grad[a:a + step] = p * (d[a:a + step, None] * inv) * keep[a:a + step, None]
+    out["dlogits"] = grad
+    order = ("loss", "pair_loss", "rewards", "logp", "dlogits") if case["op"] == "pref" else \
+        ("loss", "logp", "dlogits")
+    return {k: out[k] for k in order}
+
+
+def _exact_adam(case, s):
+    """Tensor by tensor.  Master weights and 32-bit moments in 64 bits throughout; an 8-bit
+    moment is the rounding of the fp32 moment, whose operations each round once."""
+    t = case["step"]
+    sc = _scalars(case, t, _clip_coef(case, s["sumsq"]))
+    po, padded = _padded_offsets(s["sizes"])
+    eight = case["bits"] == 8
+    key = _key(s["seed"], t)
+    rnd = lambda y: y.float().double()
+    master = s["master"].double()
+    ms = torch.zeros(padded if eight else s["total"], dtype=torch.float64, device=DEV)
+    vs = torch.zeros_like(ms)
+    for o, q, n, grp in zip(s["offs"], po, s["sizes"], s["decay"]):
+        c = sc[grp]
+        g0, p = s["grad"][o:o + n].double(), master[o:o + n].clone()
+        if eight:
+            i = torch.arange(n, device=DEV)
+            blk = q // _BLOCK + i // _BLOCK
+            em, ev = s["m_scale"][blk].double(), s["v_scale"][blk].double()
+            m0 = s["m8"][q:q + n].view(torch.float8_e4m3fn).double() * torch.exp2(em - 134)
+            cv = s["v8"][q:q + n].double()
+            e5, frac = torch.floor(cv / 8), cv % 8
+            v0 = torch.where(e5 > 0, (1 + frac / 8) * torch.exp2(e5 - 31), frac * torch.exp2(
+                torch.full_like(cv, -33.0))) * torch.exp2(ev - 127)
+        else:
+            m0, v0 = s["m"][o:o + n].double(), s["v"][o:o + n].double()
+        outs = []
+        for f in ((lambda y: y), rnd):
+            g = f(g0 * c["inv"])
+            if not case["adamw"]:
+                g = f(g + f(c["wd"] * p))
+            outs.append((f(f(c["b1"] * m0) + f(c["omb1"] * g)),
+                         f(f(c["b2"] * v0) + f(c["omb2"] * f(g * g)))))
+        m, v = outs[0]
+        master[o:o + n] = p * c["decay"] - c["step"] * (m / (v.sqrt() * c["rsbc2"] + c["eps"]))
+        if not eight:
+            ms[o:o + n], vs[o:o + n] = m, v
+            continue
+        m, v = outs[1]
+        nb = -(-n // _BLOCK)
+        top = lambda y: torch.nn.functional.pad(y.abs(), (0, nb * _BLOCK - n)).view(nb, -1).amax(1)
+        exp = lambda y: torch.where(top(y) >= 2.0 ** -126, torch.frexp(top(y))[1].double() + 126,
+                                    0.0)[i // _BLOCK]
+        em, ev = exp(m), exp(v)
+        y = rnd(m * torch.exp2(134 - em))
+        unit = torch.exp2(torch.clamp(torch.frexp(y)[1].double() - 1, min=-6.0) - 3)
+        ms[q:q + n] = torch.round(y / unit) * unit * torch.exp2(em - 134)
+        # v in units of its code's spacing, rounded up where the random fraction says so
+        y = rnd(v * torch.exp2(31 - ev)) * torch.exp2(torch.full_like(v, 96.0))
+        unit = torch.exp2(torch.clamp(torch.frexp(y)[1].double() - 1, min=-30.0) - 3)
+        r = _random16(q, nb * _BLOCK, key).reshape(-1)[:n].double()
+        k = torch.floor(y / unit)
+        up = torch.floor((y / unit - k) * 2.0 ** 20) + r * 16 >= 2.0 ** 20
+        z = torch.minimum((k + up) * unit, torch.full_like(y, 1.875))
+        z = torch.where(v > 0, torch.clamp(z, min=2.0 ** -33), 0.0)
+        vs[q:q + n] = z * torch.exp2(ev - 127)
+    out = {"master": master}
+    if "param" in s:
+        out["param"] = master
+    out["m"], out["v"] = ms, vs
+    return out
