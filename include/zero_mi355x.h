@@ -510,6 +510,221 @@ void zero_offload_destroy(zero_offload_t* off);
 int zero_adam_scalars(const zero_adam_hparams_t* hp, int64_t t_first, int64_t count,
                       double loss_scale, float* out, int32_t on_device, void* stream);
 
+/* ------------------------------------------------------------------------
+ * Fine-tuning losses: the gradients a mixed-precision step starts from
+ * ([instr] loss-scaling bullet: the loss is scaled before backward;
+ * [legal] and [instr] use cases: instruction tuning, RLHF).  Every call is
+ * asynchronous on `stream`, allocates nothing, waits for nothing and may be
+ * captured into a graph.
+ *
+ * Logits are a [rows, vocab] matrix of fp16, bf16 or fp32 elements, row r
+ * at logits + r * row_stride elements (row_stride >= vocab), aligned to
+ * their element size.  labels holds one int64 per row: a negative label
+ * masks the row (its logits are not read), a label >= vocab gives NaN.
+ * With x = logits * inv_temperature:
+ *   lse  = log sum_j exp(x_j)        logp = x_label - lse
+ * A row whose logits are all -inf has lse = logp = -inf and a zero gradient;
+ * NaN and +inf logits give NaN.  Maxima, sums and logarithms are held in
+ * fp32 or more (sums across a row's threads in fp64).
+ *
+ * loss_scale multiplies the gradients (not the losses); when loss_scale_dev
+ * is not NULL, the double it points to in device memory is used instead
+ * (zero_state_device_scale, zero_many_device_scale).
+ * ------------------------------------------------------------------------ */
+
+/* logp[r] and lse[r] of every row; both are 0 for masked rows.  lse may be
+ * NULL.  Errors: ZERO_ENULL, ZERO_EINVAL (dtype, rows < 0, vocab < 1,
+ * row_stride, inv_temperature not finite or <= 0), ZERO_EALIGN, ZERO_EHIP. */
+int zero_token_logp(const void* logits, int32_t dtype, int64_t rows, int64_t vocab,
+                    int64_t row_stride, const int64_t* labels, float inv_temperature,
+                    float* logp, float* lse, void* stream);
+
+/* The gradient of sum_r dlogp[r] * logp[r]: dlogits[r][j] = dlogp[r] *
+ * inv_temperature * ([j == label] - exp(x_j - lse[r])), rounded once to the
+ * logits' dtype.  A masked row, or one whose dlogp is 0, gets zeros.
+ * dlogits has its own row stride and may be the logits buffer itself (same
+ * address and stride); elements of a row beyond vocab are not written.
+ * Errors as zero_token_logp. */
+int zero_token_logp_grad(const void* logits, int32_t dtype, int64_t rows, int64_t vocab,
+                         int64_t row_stride, const int64_t* labels, float inv_temperature,
+                         const float* lse, const float* dlogp, void* dlogits,
+                         int64_t dlogits_stride, void* stream);
+
+enum zero_preference_kind { ZERO_PREF_SIGMOID = 0, ZERO_PREF_SQUARED = 1 };
+
+typedef struct {
+    double norm;           /* the batch loss is norm * sum of the pairs' losses */
+    float beta;            /* > 0 */
+    float label_smoothing; /* e in [0, 1), sigmoid only */
+    int32_t kind;          /* enum zero_preference_kind */
+    int32_t average;       /* 1: a sequence counts its tokens' mean, not their sum */
+} zero_preference_t;
+
+/* Preference loss of pairs of sequences from log ratios, and its gradient.
+ * Sequence s holds the tokens seq_offsets[s] .. seq_offsets[s+1] - 1 (2 *
+ * pairs + 1 non-decreasing int64 in device memory, from 0 to rows);
+ * sequences 2i and 2i+1 are pair i's chosen and rejected answers.  With
+ * D_s the sum (or mean) over the sequence's unmasked tokens of logp -
+ * ref_logp (an empty sequence: 0) and delta = D_2i - D_2i+1:
+ *   sigmoid  h = beta * delta,
+ *            L = -(1 - e) log sigmoid(h) - e log sigmoid(-h)
+ *   squared  L = (delta - 1 / (2 beta))^2
+ * Outputs: pair_loss[i] = L, rewards[2i], [2i+1] = beta * D, loss[0] = norm
+ * * sum L, dlogp[t] = loss_scale * norm * dL/dlogp_t (0 for masked tokens).
+ * Tokens are masked where labels[t] < 0 (labels NULL: none); ref_logp NULL
+ * stands for zeros.  Sums are in fp64, in a fixed order.
+ * Errors: ZERO_ENULL, ZERO_EINVAL (sizes, cfg, loss_scale), ZERO_EALIGN,
+ * ZERO_EHIP. */
+int zero_preference_loss(const float* logp, const float* ref_logp, const int64_t* labels,
+                         int64_t rows, const int64_t* seq_offsets, int64_t pairs,
+                         const zero_preference_t* cfg, double loss_scale,
+                         const double* loss_scale_dev, float* loss, float* pair_loss,
+                         float* rewards, float* dlogp, void* stream);
+
+typedef struct {
+    double norm;           /* the batch loss is norm * the weighted sum over tokens */
+    float clip_low;        /* in [0, 1) */
+    float clip_high;       /* >= 0 */
+    float kl_coef;         /* >= 0; must be 0 when ref_logp is NULL */
+    float inv_temperature; /* > 0 */
+} zero_policy_t;
+
+/* Clipped policy loss with a KL term, from the logits to their gradient in
+ * one call.  Per unmasked token, with r = exp(logp - old_logp), A =
+ * advantage, q = ref_logp - logp and w = weight (NULL: 1):
+ *   pg = -min(r A, clip(r, 1 - clip_low, 1 + clip_high) A)
+ *   kl = exp(q) - q - 1          (0 when ref_logp is NULL)
+ *   dlogp = -A r [r A <= clip(r) A] + kl_coef (1 - exp(q))
+ * A token of weight 0 adds nothing to the sums and has a zero gradient.
+ * Outputs: logp[r] (0 for masked rows), terms[4r .. 4r+3] = pg, kl, whether
+ * the clip was active, w (all 0 for masked rows), loss[0..3] = norm * sum w
+ * (pg + kl_coef kl), norm * sum w pg, norm * sum w kl, norm * sum w clipped,
+ * and dlogits = loss_scale * norm * w * dlogp * inv_temperature * ([j ==
+ * label] - exp(x_j - lse)), as zero_token_logp_grad lays it out (in place
+ * too).  Token terms are formed in fp64.  terms must be 16-byte aligned.
+ * Errors: ZERO_ENULL, ZERO_EINVAL, ZERO_EALIGN, ZERO_EHIP. */
+int zero_policy_loss(const void* logits, int32_t dtype, int64_t rows, int64_t vocab,
+                     int64_t row_stride, const int64_t* labels, const float* old_logp,
+                     const float* ref_logp, const float* advantage, const float* weight,
+                     const zero_policy_t* cfg, double loss_scale, const double* loss_scale_dev,
+                     float* logp, float* terms, float* loss, void* dlogits,
+                     int64_t dlogits_stride, void* stream);
+
+/* ------------------------------------------------------------------------
+ * AdamW over many tensors where they lie: the update of zero_adam_step with
+ * no flat copy of the gradients or the state, with the moments in fp32 or
+ * in 8 bits, clipped by the global norm, gated and loss-scaled on the
+ * device.
+ *
+ * States in 8 bits (state_bits = 8).  Each tensor is cut into blocks of 256
+ * elements from its own start (the last one may be short).  A block keeps,
+ * for each moment, one byte E: the exponent field (bits 30..23) of the
+ * largest |value| in it, NaNs aside.
+ *   exp_avg     one e4m3 code per element (1 sign, 4 exponent, 3 fraction
+ *               bits, 0x7F = NaN): value = code * 2^(E - 134), rounded to
+ *               nearest even.
+ *   exp_avg_sq  one unsigned code c per element, 5 exponent and 3 fraction
+ *               bits: value = float_with_bits(c << 20) * 2^(E - 31), rounded
+ *               stochastically, never from above 0 to 0.
+ * Nearest rounding would hold the second moment still: a step changes it
+ * by about 1 - beta2 of itself, far below half a code.  The stochastic
+ * rounding adds 16 random bits (of the 20 that are dropped) from a counter
+ * hash of the seed, the step and the element, so a resumed run repeats the
+ * same bits.  All-zero bytes stand for zero moments.  Infinite or NaN first
+ * moments become NaN.  6 bytes of state per parameter instead of 12.
+ *
+ * Devices, threads and streams: as a plan.  A handle owns a device table of
+ * its tensors and a small device block, made by zero_many_bind; the tensors
+ * stay the caller's and must outlive the work enqueued on them.
+ * ------------------------------------------------------------------------ */
+typedef struct zero_many zero_many_t; /* opaque, library owned */
+
+#define ZERO_MANY_BLOCK 256      /* elements that share a scale */
+#define ZERO_MANY_MAX_GROUPS 16  /* hyperparameter groups */
+
+typedef struct {
+    int64_t total_numel;  /* sum of the tensors' elements */
+    int64_t padded_numel; /* the same with each tensor rounded up to whole blocks */
+    int64_t state_bytes;  /* bytes of both moments and their scales */
+    int32_t n_tensors;
+    int32_t n_groups;
+    int32_t state_bits;
+    int32_t _pad;
+} zero_many_info_t;
+
+/* Creates a handle for n_tensors tensors of numels[i] >= 0 elements, tensor
+ * i in hyperparameter group groups[i] (NULL: all in group 0) of n_groups (1
+ * .. ZERO_MANY_MAX_GROUPS); state_bits is 8 or 32.  Host only.
+ * Errors: ZERO_ENULL, ZERO_EINVAL, ZERO_ENOMEM. */
+int zero_many_create(const int64_t* numels, const int32_t* groups, int32_t n_tensors,
+                     int32_t n_groups, int32_t state_bits, zero_many_t** out);
+int zero_many_info(const zero_many_t* many, zero_many_info_t* out);
+/* First element of each tensor in the padded order (a multiple of 256);
+ * returns n_tensors or a negative error.  out may be NULL when cap is 0. */
+int64_t zero_many_offsets(const zero_many_t* many, int64_t* out, int64_t cap);
+void zero_many_destroy(zero_many_t* many); /* NULL is a no-op */
+
+/* One device pointer per tensor, arrays in host memory.  grad[i] may be
+ * NULL: the tensor has no gradient and is left alone.  master and the
+ * moments may be NULL as a whole when only zero_many_grad_norm is called;
+ * param may be NULL (no half copy).  exp_avg and exp_avg_sq point to floats
+ * (32 bits) or code bytes; the scale arrays, one byte per block, are for 8
+ * bits only.  Pointers are aligned to their element; 16-byte aligned
+ * fp32 and gradients, 8-byte aligned half gradients and parameters and
+ * 4-byte aligned codes take the wide path. */
+typedef struct {
+    const void* const* grad;
+    float* const* master;
+    void* const* exp_avg;
+    void* const* exp_avg_sq;
+    uint8_t* const* exp_avg_scale;
+    uint8_t* const* exp_avg_sq_scale;
+    void* const* param;
+    int32_t grad_dtype;  /* ZERO_F16, ZERO_BF16 or ZERO_F32, of every tensor */
+    int32_t param_dtype; /* ZERO_F16 or ZERO_BF16 */
+} zero_many_buffers_t;
+
+/* Hands the tensors to the handle (again after any of them moved); waits
+ * for `stream`, and cannot be captured.  Errors: ZERO_ENULL, ZERO_EINVAL,
+ * ZERO_EALIGN, ZERO_ESTATE (capturing, or another device), ZERO_EHIP,
+ * ZERO_ENOMEM. */
+int zero_many_bind(zero_many_t* many, const zero_many_buffers_t* buffers, void* stream);
+
+/* Step count (= applied_steps), loss scaler and seed into the handle's
+ * device state (waits), and back; as zero_state_upload / _download. */
+int zero_many_state_upload(zero_many_t* many, int64_t applied_steps, const zero_scaler_t* scaler,
+                           uint64_t seed, void* stream);
+int zero_many_state_download(zero_many_t* many, int64_t* applied_steps, zero_scaler_t* scaler,
+                             int32_t* last_flag, int64_t* skipped_steps, void* stream);
+int zero_many_device_scale(zero_many_t* many, const double** out);
+
+/* sumsq[0] = the sum of all squared gradients, as they are (scaled), in
+ * fp64 and in a fixed order; flag[0] = 1 if any is inf or NaN, else 0 (both
+ * device memory; across ranks: add the sums, take the largest flag).
+ * Asynchronous; capturable.  Errors: ZERO_ENULL, ZERO_EALIGN, ZERO_ESTATE
+ * (not bound), ZERO_EHIP. */
+int zero_many_grad_norm(zero_many_t* many, double* sumsq, int32_t* flag, void* stream);
+
+/* One step of every tensor, hp[g] for group g, at t + 1 of the device
+ * state, asynchronous and capturable.  The step is skipped (and the loss
+ * scale backs off) when flag is not NULL and holds 1, or when sumsq holds
+ * inf or NaN.  With sumsq given and max_norm > 0, gradients are
+ * multiplied by min(1, max_norm / (sqrt(sumsq) / scale + 1e-6)); that and
+ * 1/scale form one fp32 factor.  Everything else per element is the update
+ * of zero_adam_step, in its order.  norm_out (NULL: none) receives
+ * sqrt(sumsq) / scale and the clip factor.  Errors: ZERO_ENULL, ZERO_EINVAL
+ * (hyperparameters, n_groups, max_norm), ZERO_EALIGN, ZERO_ESTATE (not
+ * bound, or no device state), ZERO_EHIP. */
+int zero_many_adam_step(zero_many_t* many, const zero_adam_hparams_t* hp, int32_t n_groups,
+                        const int32_t* flag, const double* sumsq, double max_norm,
+                        float* norm_out, void* stream);
+
+/* The moments as fp32 in the padded order (padded_numel floats each, 16-byte
+ * aligned; zeros behind each tensor's end), for checkpoints and
+ * inspection.  Either may be NULL.  Errors: ZERO_ENULL, ZERO_EALIGN,
+ * ZERO_ESTATE, ZERO_EHIP. */
+int zero_many_state_values(zero_many_t* many, float* exp_avg, float* exp_avg_sq, void* stream);
+
 /* Message of the calling thread's last error ("" if none). */
 const char* zero_last_error(void);
 

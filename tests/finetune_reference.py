@@ -1,0 +1,221 @@
+"""Plain statements of the fine-tuning operators, for their tests: the losses
+in 64 bits, the many-tensor AdamW step with every operation rounded once to
+fp32 (the order the header pins), and the 8-bit moments from their format.
+Shares no code with the library."""
+from __future__ import annotations
+
+import math
+
+import numpy as np
+import torch
+
+BLOCK = 256
+
+
+# ------------------------------------------------------------------- losses
+def f32(x) -> float:
+    return float(np.float32(x))
+
+
+def token_logp(logits, labels, inv_t=1.0):
+    """(x, logp, lse) in fp64; masked rows 0; a row of -inf alone: -inf, -inf."""
+    x = logits.double() * f32(inv_t)
+    vocab = x.shape[1]
+    top = x.amax(1)
+    base = torch.where(top == -math.inf, torch.zeros_like(top), top)
+    lse = base + (x - base[:, None]).exp().sum(1).log()
+    at = x.gather(1, labels.clamp(0, vocab - 1)[:, None])[:, 0]
+    logp = torch.where(lse == -math.inf, torch.full_like(lse, -math.inf), at - lse)
+    logp = torch.where(labels >= vocab, torch.full_like(lse, math.nan), logp)
+    live = labels >= 0
+    return x, torch.where(live, logp, 0.0), torch.where(live, lse, 0.0)
+
+
+def logits_grad(x, labels, lse, dlogp, inv_t=1.0):
+    """dlogits in fp64 of sum(dlogp * logp)."""
+    g = torch.where(labels >= 0, dlogp.double() * f32(inv_t), 0.0)
+    p = (x - lse[:, None]).exp()
+    d = -p
+    inside = (labels >= 0) & (labels < x.shape[1])
+    rows = torch.nonzero(inside)[:, 0]
+    d[rows, labels[rows]] += 1.0
+    d = d * g[:, None]
+    return torch.where(((g == 0) | (lse == -math.inf))[:, None], torch.zeros_like(d), d)
+
+
+def softplus(y: float) -> float:
+    return max(y, 0.0) + math.log1p(math.exp(-abs(y)))
+
+
+def sigmoid(y: float) -> float:
+    if y >= 0:
+        return 1.0 / (1.0 + math.exp(-y))
+    return math.exp(y) / (1.0 + math.exp(y))
+
+
+def preference(logp, ref, labels, cu, kind="sigmoid", beta=0.1, smoothing=0.0, average=False,
+               norm=1.0, scale=1.0):
+    """(loss, pair_loss, rewards, dlogp) in fp64, pair by pair."""
+    b, e = f32(beta), f32(smoothing)
+    n = len(logp)
+    live = np.ones(n, bool) if labels is None else np.asarray(labels) >= 0
+    diff = np.asarray(logp, np.float64) - (0.0 if ref is None else np.asarray(ref, np.float64))
+    dlogp = np.zeros(n)
+    losses, rewards = [], []
+    for i in range(len(cu) // 2):
+        d, cnt, span = [], [], []
+        for s in (0, 1):
+            a, z = int(cu[2 * i + s]), int(cu[2 * i + s + 1])
+            keep = np.arange(a, z)[live[a:z]]
+            cnt.append(max(len(keep), 1) if average else 1)
+            d.append(math.fsum(diff[keep]) / cnt[-1])
+            span.append(keep)
+        delta = d[0] - d[1]
+        if kind == "squared":
+            u = delta - 1.0 / (2.0 * b)
+            loss, slope = u * u, 2.0 * u
+        else:
+            h = b * delta
+            loss = (1 - e) * softplus(-h) + e * softplus(h)
+            slope = b * (e * sigmoid(h) - (1 - e) * sigmoid(-h))
+        losses.append(loss)
+        rewards.append([b * d[0], b * d[1]])
+        for s, sign in ((0, 1.0), (1, -1.0)):
+            dlogp[span[s]] = sign * slope * norm * scale / cnt[s]
+    return (norm * math.fsum(losses), np.array(losses), np.array(rewards).reshape(-1, 2), dlogp)
+
+
+def policy(logp, labels, old, ref, adv, weight, lo=0.2, hi=0.2, kl_coef=0.0, norm=1.0, scale=1.0):
+    """(loss[4], terms[rows, 4], dlogp) in fp64 from fp64 logp (torch, CPU)."""
+    live = labels >= 0
+    w = torch.ones_like(logp) if weight is None else weight.double()
+    w = torch.where(live, w, 0.0)
+    a = adv.double()
+    r = (logp - old.double()).exp()
+    kept, cut = r * a, r.clamp(1 - f32(lo), 1 + f32(hi)) * a
+    clipped = kept > cut
+    pg = -torch.where(clipped, cut, kept)
+    q = torch.zeros_like(logp) if ref is None else ref.double() - logp
+    kl = torch.expm1(q) - q
+    d = torch.where(clipped, 0.0, -kept) - f32(kl_coef) * torch.expm1(q)
+    on = w != 0
+    terms = torch.stack([pg, kl, clipped.double(), w], 1)
+    terms = torch.where(on[:, None], terms, torch.zeros_like(terms))
+    s = [norm * math.fsum((terms[:, 3] * terms[:, k]).tolist()) for k in range(3)]
+    loss = np.array([s[0] + f32(kl_coef) * s[1], *s])
+    return loss, terms, torch.where(on, d * w, 0.0) * (scale * norm)
+
+
+# ---------------------------------------------------------- 8-bit moments
+def e4m3_values():
+    """The value of each of the 256 codes (0x7F and 0xFF: NaN)."""
+    out = np.zeros(256)
+    for c in range(256):
+        e, f = (c >> 3) & 15, c & 7
+        v = (1 + f / 8) * 2.0 ** (e - 7) if e else f / 8 * 2.0 ** -6
+        if e == 15 and f == 7:
+            v = math.nan
+        out[c] = -v if c & 128 else v
+    return out
+
+
+def blocks_of(x):
+    n = -(-len(x) // BLOCK)
+    out = np.zeros(n * BLOCK, x.dtype)
+    out[:len(x)] = x
+    return out.reshape(n, BLOCK)
+
+
+def exponents(x):
+    """One byte per block: the exponent field of the largest |x|, NaNs aside."""
+    a = np.abs(blocks_of(x.astype(np.float32)))
+    top = np.where(np.isnan(a), np.float32(0), a).max(1)
+    return (top.view(np.uint32) >> 23).astype(np.uint8)
+
+
+def scaled(x, e):
+    """x 2^e rounded once to fp32 (x fp32, e per element)."""
+    with np.errstate(over="ignore", under="ignore", invalid="ignore"):
+        return np.ldexp(x.astype(np.float64), e.astype(np.int64)).astype(np.float32)
+
+
+def per_element(scales, n):
+    return np.repeat(scales.astype(np.int64), BLOCK)[:n]
+
+
+def pack_m(m):
+    scale = exponents(m)
+    y = scaled(m, 134 - per_element(scale, len(m)))
+    codes = torch.from_numpy(y).to(torch.float8_e4m3fn).view(torch.uint8).numpy().copy()
+    codes[~np.isfinite(y)] = 0x7F
+    return codes, scale
+
+
+def unpack_m(codes, scale):
+    return scaled(e4m3_values()[codes].astype(np.float32),
+                  per_element(scale, len(codes)) - 134)
+
+
+def key_of(seed, t):
+    m = (1 << 64) - 1
+    z = (seed + t * 0x9E3779B97F4A7C15) & m
+    z = ((z ^ (z >> 30)) * 0xBF58476D1CE4E5B9) & m
+    z = ((z ^ (z >> 27)) * 0x94D049BB133111EB) & m
+    return (z ^ (z >> 31)) & 0xFFFFFFFF
+
+
+def random16(first, n, key):
+    """The 16 random bits of elements first .. first + n - 1 of the padded order."""
+    low = np.uint64(0xFFFFFFFF)
+    elem = np.arange(first, first + n, dtype=np.uint64)
+    pair = elem >> np.uint64(1)
+    hi = ((pair >> np.uint64(32)) * np.uint64(0x6A09E667)) & low
+    x = ((pair & low) * np.uint64(0x9E3779B1) + (np.uint64(key) ^ hi)) & low
+    x ^= x >> np.uint64(16)
+    x = (x * np.uint64(0xBB67AE85)) & low
+    x ^= x >> np.uint64(15)
+    return np.where(elem & np.uint64(1), x >> np.uint64(16), x & np.uint64(0xFFFF)).astype(np.int64)
+
+
+def pack_v(v, first, key):
+    scale = exponents(v)
+    y = scaled(v, 31 - per_element(scale, len(v)))
+    bits = (y.view(np.uint32) & np.uint32(0x7FFFFFFF)).astype(np.int64)
+    code = np.minimum((bits + 16 * random16(first, len(v), key)) >> 20, 255)
+    zero = (v.view(np.uint32) & np.uint32(0x7FFFFFFF)) == 0
+    return np.where(zero, 0, np.maximum(code, 1)).astype(np.uint8), scale
+
+
+def unpack_v(codes, scale):
+    return scaled((codes.astype(np.uint32) << 20).view(np.float32),
+                  per_element(scale, len(codes)) - 31)
+
+
+# ------------------------------------------------------------- AdamW step
+def scalars(hp, t, scale, coef=1.0):
+    f = np.float32
+    return dict(inv=f(coef / scale), b1=f(hp.beta1), omb1=f(1 - hp.beta1), b2=f(hp.beta2),
+                omb2=f(1 - hp.beta2), step=f(hp.lr / (1 - hp.beta1 ** t)),
+                rsbc2=f(1 / math.sqrt(1 - hp.beta2 ** t)), eps=f(hp.eps),
+                decay=f(1 - hp.lr * hp.weight_decay) if hp.adamw else f(1),
+                wd=f(hp.weight_decay))
+
+
+def adam(g, p, m, v, c, adamw):
+    """One step on fp32 arrays, each operation rounded once."""
+    with np.errstate(over="ignore", under="ignore", invalid="ignore"):
+        gu = g * c["inv"]
+        if not adamw:
+            gu = gu + c["wd"] * p
+        m = c["b1"] * m + c["omb1"] * gu
+        v = c["b2"] * v + c["omb2"] * (gu * gu)
+        d = np.sqrt(v) * c["rsbc2"] + c["eps"]
+        p = p * c["decay"] - c["step"] * (m / d)
+    assert p.dtype == np.float32 and m.dtype == np.float32 and v.dtype == np.float32
+    return p, m, v
+
+
+def clip_coef(sumsq, scale, max_norm):
+    if not max_norm:
+        return 1.0
+    return min(1.0, max_norm / (math.sqrt(sumsq) / scale + 1e-6))

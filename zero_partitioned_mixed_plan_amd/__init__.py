@@ -42,6 +42,24 @@ and ZeRO-Offload's host-side update (host buffers: numpy arrays or CPU tensors):
             n_threads=None)     .submit / .wait_params / .drain / .stats / .close
                                 (zero_offload_* : the pipelined offloaded step with the
                                  one-step delayed parameter update)
+
+and the losses of fine-tuning, from the logits to their (loss-scaled) gradient:
+
+    zero_token_logp(logits, labels, logp, lse=None, inv_temperature=1.0, stream=None)
+    zero_token_logp_grad(logits, labels, lse, dlogp, dlogits, inv_temperature=1.0, stream=None)
+    zero_preference_loss(logp, ref_logp, seq_offsets, loss, pair_loss, rewards, dlogp, ...)
+    zero_policy_loss(logits, labels, old_logp, advantage, dlogits, logp, terms, loss, ...)
+
+and AdamW over many tensors where they lie, moments in fp32 or 8 bits:
+
+    zero_many_create(numels, state_bits=8, groups=None, n_groups=1) -> ManyTensors
+    zero_many_bind(many, grads, master=None, exp_avg=None, exp_avg_sq=None,
+                   exp_avg_scale=None, exp_avg_sq_scale=None, param=None, stream=None)
+    zero_many_state_upload / zero_many_state_download / zero_many_device_scale
+    zero_many_grad_norm(many, sumsq, flag, stream=None)
+    zero_many_adam_step(many, hparams, flag=None, sumsq=None, max_norm=0.0, norm_out=None,
+                        stream=None)
+    zero_many_state_values(many, exp_avg=None, exp_avg_sq=None, stream=None)
 """
 from __future__ import annotations
 
@@ -63,7 +81,11 @@ __all__ = ["Plan", "release_all", "AdamHParams", "LossScaler", "DeviceStepState"
            "zero_adam_step_async", "zero_state_download", "zero_state_device_scale",
            "zero_adam_step_noalloc",
            "zero_cpu_adam_step", "zero_cpu_isa", "default_host_threads", "zero_adam_scalars", "SCALAR_FIELDS",
-           "Offload", "zero_last_error", "ZERO_F16",
+           "Offload", "zero_token_logp", "zero_token_logp_grad", "zero_preference_loss",
+           "zero_policy_loss", "ManyTensors", "zero_many_create", "zero_many_bind",
+           "zero_many_state_upload", "zero_many_state_download", "zero_many_device_scale",
+           "zero_many_grad_norm", "zero_many_adam_step", "zero_many_state_values",
+           "zero_last_error", "ZERO_F16",
            "ZERO_BF16", "ZERO_F32"]
 
 
@@ -147,16 +169,20 @@ class LossScaler:
 # everything is still alive.
 _LIVE_PLANS: "weakref.WeakSet[Plan]" = weakref.WeakSet()
 _LIVE_OFFLOADS: "weakref.WeakSet[Offload]" = weakref.WeakSet()
+_LIVE_MANY: "weakref.WeakSet[ManyTensors]" = weakref.WeakSet()
 
 
 def release_all() -> None:
     """Release every live offload pipeline (its worker thread is joined),
-    then every live plan (its device block and pinned mirror are freed).
+    then every live plan and tensor list (their device blocks and pinned
+    mirrors are freed).
     Registered with atexit; callers may also call it at the end of a run."""
     for o in list(_LIVE_OFFLOADS):
         o.close()
     for p in list(_LIVE_PLANS):
         p.close()
+    for w in list(_LIVE_MANY):
+        w.close()
 
 
 atexit.register(release_all)
@@ -631,6 +657,342 @@ class Offload:
         if self._finalizing():
             return
         self.close()
+
+
+# ------------------------------------------------------------ fine-tuning losses
+def _matrix(t, name: str, dtypes):
+    """A [rows, vocab] device matrix with unit column stride: (rows, vocab, row stride)."""
+    torch = _torch()
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a device tensor")
+    if t.dim() != 2:
+        raise ValueError(f"{name} must be a [rows, vocab] matrix, got {t.dim()} dimensions")
+    if t.dtype not in dtypes:
+        raise TypeError(f"{name} has dtype {t.dtype}, expected one of {dtypes}")
+    rows, vocab = t.shape
+    if vocab > 1 and t.stride(1) != 1:
+        raise ValueError(f"{name} must have unit stride along the vocabulary")
+    stride = t.stride(0) if rows > 1 else max(vocab, 1)
+    if stride < vocab:
+        raise ValueError(f"{name} has overlapping rows")
+    return rows, vocab, stride
+
+
+def _logits_and_labels(logits, labels):
+    torch = _torch()
+    rows, vocab, stride = _matrix(logits, "logits", _grad_dtypes())
+    _require(labels, "labels", rows, (torch.int64,))
+    return rows, vocab, stride
+
+
+def _floats(rows: int, **tensors) -> None:
+    torch = _torch()
+    for name, t in tensors.items():
+        _require(t, name, rows, (torch.float32,))
+
+
+def _dlogits(dlogits, logits):
+    _, _, stride = _matrix(dlogits, "dlogits", (logits.dtype,))
+    if dlogits.shape != logits.shape:
+        raise ValueError(f"dlogits has shape {tuple(dlogits.shape)}, logits {tuple(logits.shape)}")
+    return stride
+
+
+def _ptr(t):
+    return None if t is None else t.data_ptr()
+
+
+def zero_token_logp(logits, labels, logp, lse=None, inv_temperature: float = 1.0,
+                    stream=None) -> None:
+    """logp[r] = the log-probability of labels[r] (int64; negative: masked, 0) under
+    softmax(logits[r] * inv_temperature); lse[r] = the row's log-sum-exp."""
+    rows, vocab, stride = _logits_and_labels(logits, labels)
+    _floats(rows, logp=logp)
+    if lse is not None:
+        _floats(rows, lse=lse)
+    check(lib.zero_token_logp(logits.data_ptr(), _dtype_code(logits), rows, vocab, stride,
+                              labels.data_ptr(), float(inv_temperature), logp.data_ptr(),
+                              _ptr(lse), _stream_handle(stream, logits.device)),
+          "zero_token_logp")
+
+
+def zero_token_logp_grad(logits, labels, lse, dlogp, dlogits, inv_temperature: float = 1.0,
+                         stream=None) -> None:
+    """dlogits = the gradient of sum(dlogp * logp) to the logits, in their dtype; dlogits may
+    be the logits tensor itself."""
+    rows, vocab, stride = _logits_and_labels(logits, labels)
+    _floats(rows, lse=lse, dlogp=dlogp)
+    check(lib.zero_token_logp_grad(logits.data_ptr(), _dtype_code(logits), rows, vocab, stride,
+                                   labels.data_ptr(), float(inv_temperature), lse.data_ptr(),
+                                   dlogp.data_ptr(), dlogits.data_ptr(), _dlogits(dlogits, logits),
+                                   _stream_handle(stream, logits.device)),
+          "zero_token_logp_grad")
+
+
+_PREFERENCE_KINDS = {"sigmoid": 0, "squared": 1}
+
+
+def zero_preference_loss(logp, ref_logp, seq_offsets, loss, pair_loss, rewards, dlogp,
+                         labels=None, kind: str = "sigmoid", beta: float = 0.1,
+                         label_smoothing: float = 0.0, average: bool = False,
+                         norm: Optional[float] = None, loss_scale: float = 1.0,
+                         loss_scale_dev: Optional[int] = None, stream=None) -> None:
+    """Preference loss of pairs from per-token log-probabilities, and its gradient dlogp.
+
+    seq_offsets: int64 device tensor of 2 * pairs + 1 token offsets; sequences 2i and 2i + 1
+    are pair i's chosen and rejected answers.  loss [1] = norm (default 1 / pairs) times the
+    sum of pair_loss [pairs]; rewards [pairs, 2].  labels: tokens with a negative label are
+    masked.  ref_logp None stands for zeros.  loss_scale_dev: device address of a double
+    (zero_state_device_scale, zero_many_device_scale) used in place of loss_scale."""
+    torch = _torch()
+    if kind not in _PREFERENCE_KINDS:
+        raise ValueError(f"kind must be one of {sorted(_PREFERENCE_KINDS)}, got {kind!r}")
+    _require(seq_offsets, "seq_offsets", 1, (torch.int64,))
+    if seq_offsets.numel() % 2 != 1:
+        raise ValueError("seq_offsets must hold 2 * pairs + 1 offsets")
+    pairs = seq_offsets.numel() // 2
+    _floats(0, logp=logp)
+    rows = logp.numel()
+    _floats(rows, dlogp=dlogp)
+    _floats(1, loss=loss)
+    _floats(pairs, pair_loss=pair_loss)
+    _floats(2 * pairs, rewards=rewards)
+    if ref_logp is not None:
+        _floats(rows, ref_logp=ref_logp)
+    if labels is not None:
+        _require(labels, "labels", rows, (torch.int64,))
+    cfg = _abi.zero_preference_t(1.0 / max(pairs, 1) if norm is None else float(norm),
+                                 float(beta), float(label_smoothing), _PREFERENCE_KINDS[kind],
+                                 1 if average else 0)
+    check(lib.zero_preference_loss(logp.data_ptr(), _ptr(ref_logp), _ptr(labels), rows,
+                                   seq_offsets.data_ptr(), pairs, ctypes.byref(cfg),
+                                   float(loss_scale), loss_scale_dev, loss.data_ptr(),
+                                   pair_loss.data_ptr(), rewards.data_ptr(), dlogp.data_ptr(),
+                                   _stream_handle(stream, logp.device)), "zero_preference_loss")
+
+
+def zero_policy_loss(logits, labels, old_logp, advantage, dlogits, logp, terms, loss,
+                     ref_logp=None, weight=None, clip_low: float = 0.2, clip_high: float = 0.2,
+                     kl_coef: float = 0.0, norm: float = 1.0, inv_temperature: float = 1.0,
+                     loss_scale: float = 1.0, loss_scale_dev: Optional[int] = None,
+                     stream=None) -> None:
+    """Clipped policy loss with a KL term, from the logits to their gradient in one call.
+
+    loss [4] = norm * sum over tokens of weight * (loss, policy part, KL, clipped); terms
+    [rows, 4] = each token's policy part, KL, clipped, weight; dlogits may be the logits
+    tensor itself.  loss_scale_dev as in zero_preference_loss."""
+    rows, vocab, stride = _logits_and_labels(logits, labels)
+    _floats(rows, old_logp=old_logp, advantage=advantage, logp=logp)
+    _floats(4 * rows, terms=terms)
+    _floats(4, loss=loss)
+    if ref_logp is not None:
+        _floats(rows, ref_logp=ref_logp)
+    if weight is not None:
+        _floats(rows, weight=weight)
+    cfg = _abi.zero_policy_t(float(norm), float(clip_low), float(clip_high), float(kl_coef),
+                             float(inv_temperature))
+    check(lib.zero_policy_loss(logits.data_ptr(), _dtype_code(logits), rows, vocab, stride,
+                               labels.data_ptr(), old_logp.data_ptr(), _ptr(ref_logp),
+                               advantage.data_ptr(), _ptr(weight), ctypes.byref(cfg),
+                               float(loss_scale), loss_scale_dev, logp.data_ptr(),
+                               terms.data_ptr(), loss.data_ptr(), dlogits.data_ptr(),
+                               _dlogits(dlogits, logits), _stream_handle(stream, logits.device)),
+          "zero_policy_loss")
+
+
+# ------------------------------------------------------------ many tensors
+class ManyTensors:
+    """A list of tensors that step together (owned handle, released like a Plan).  The
+    tensors given to zero_many_bind are kept alive until the next bind or close()."""
+
+    BLOCK = 256  # elements that share one scale of the 8-bit moments
+
+    def __init__(self, handle: int, numels: Sequence[int]):
+        self._h = ctypes.c_void_p(handle)
+        self.numels = [int(n) for n in numels]
+        info = _abi.zero_many_info_t()
+        check(lib.zero_many_info(self._h, ctypes.byref(info)), "zero_many_info")
+        self.info = info
+        self._tensors = None
+        _LIVE_MANY.add(self)
+
+    _destroy = staticmethod(lib.zero_many_destroy)
+    _finalizing = staticmethod(sys.is_finalizing)
+
+    def close(self) -> None:
+        h = getattr(self, "_h", None)
+        if h is not None and h.value:
+            self._destroy(h)
+        self._h = ctypes.c_void_p()
+        self._tensors = None
+
+    def __del__(self):
+        if self._finalizing():
+            return
+        self.close()
+
+    @property
+    def handle(self) -> ctypes.c_void_p:
+        return self._h
+
+    total_numel = property(lambda self: int(self.info.total_numel))
+    padded_numel = property(lambda self: int(self.info.padded_numel))
+    state_bytes = property(lambda self: int(self.info.state_bytes))
+    n_groups = property(lambda self: int(self.info.n_groups))
+    state_bits = property(lambda self: int(self.info.state_bits))
+
+    def offsets(self) -> List[int]:
+        """First element of each tensor in the padded order of zero_many_state_values."""
+        n = len(self.numels)
+        arr = (ctypes.c_int64 * max(n, 1))()
+        check(lib.zero_many_offsets(self._h, arr, n), "zero_many_offsets")
+        return list(arr[:n])
+
+    def blocks(self) -> List[int]:
+        """Scales (one byte each) of each tensor's 8-bit moments."""
+        return [-(-n // self.BLOCK) for n in self.numels]
+
+
+def zero_many_create(numels: Sequence[int], state_bits: int = 8,
+                     groups: Optional[Sequence[int]] = None, n_groups: int = 1) -> ManyTensors:
+    n = len(numels)
+    if groups is not None and len(groups) != n:
+        raise ValueError(f"need {n} groups, got {len(groups)}")
+    arr = (ctypes.c_int64 * max(n, 1))(*[int(k) for k in numels])
+    grp = None if groups is None else (ctypes.c_int32 * max(n, 1))(*[int(g) for g in groups])
+    h = ctypes.c_void_p()
+    check(lib.zero_many_create(arr, grp, n, int(n_groups), int(state_bits), ctypes.byref(h)),
+          "zero_many_create")
+    return ManyTensors(h.value, numels)
+
+
+def _pointers(tensors, name: str, numels, dtypes, may_be_none: bool = False):
+    """(pointer array, dtype) of one device tensor per entry, all of one dtype."""
+    if len(tensors) != len(numels):
+        raise ValueError(f"need {len(numels)} entries in {name}, got {len(tensors)}")
+    dtype = None
+    ptrs = (ctypes.c_void_p * max(len(tensors), 1))()
+    for i, t in enumerate(tensors):
+        if t is None and may_be_none:
+            continue
+        _require(t, f"{name}[{i}]", int(numels[i]), dtypes if dtype is None else (dtype,))
+        dtype = t.dtype
+        ptrs[i] = t.data_ptr()
+    return ptrs, dtype
+
+
+def zero_many_bind(many: ManyTensors, grads, master=None, exp_avg=None, exp_avg_sq=None,
+                   exp_avg_scale=None, exp_avg_sq_scale=None, param=None, stream=None) -> None:
+    """Hand the tensors over (again after any of them moved; waits for the stream).
+
+    One entry per tensor in each list: grads (fp16, bf16 or fp32; None: left alone), master
+    (fp32), the moments (fp32, or uint8 codes with one uint8 scale per 256 elements), param
+    (fp16 or bf16, optional).  grads alone are enough for zero_many_grad_norm."""
+    torch = _torch()
+    f32, u8 = (torch.float32,), (torch.uint8,)
+    state = u8 if many.state_bits == 8 else f32
+    b = _abi.zero_many_buffers_t()
+    keep = {}
+
+    def put(field, tensors, numels, dtypes, none=False):
+        if tensors is None:
+            return None
+        tensors = list(tensors)
+        keep[field], dtype = _pointers(tensors, field, numels, dtypes, none)
+        keep[field + "_tensors"] = tensors
+        setattr(b, field, ctypes.cast(keep[field], ctypes.c_void_p))
+        return dtype
+
+    gdt = put("grad", grads, many.numels, _grad_dtypes(), True)
+    put("master", master, many.numels, f32)
+    put("exp_avg", exp_avg, many.numels, state)
+    put("exp_avg_sq", exp_avg_sq, many.numels, state)
+    put("exp_avg_scale", exp_avg_scale, many.blocks(), u8)
+    put("exp_avg_sq_scale", exp_avg_sq_scale, many.blocks(), u8)
+    pdt = put("param", param, many.numels, (torch.float16, torch.bfloat16))
+    codes = {torch.float16: ZERO_F16, torch.bfloat16: ZERO_BF16, torch.float32: ZERO_F32}
+    b.grad_dtype = codes.get(gdt, ZERO_F32)
+    b.param_dtype = codes.get(pdt, ZERO_BF16 if param is not None else 0)
+    check(lib.zero_many_bind(many.handle, ctypes.byref(b), _current(stream)), "zero_many_bind")
+    many._tensors = keep
+
+
+def _current(stream):
+    torch = _torch()
+    return _stream_handle(stream, torch.device("cuda", torch.cuda.current_device()))
+
+
+def zero_many_state_upload(many: ManyTensors, applied_steps: int, scaler: LossScaler,
+                           seed: int = 0, stream=None) -> None:
+    """Load t (= applied_steps), the scaler and the rounding seed into the handle's device
+    state (waits)."""
+    check(lib.zero_many_state_upload(many.handle, int(applied_steps), ctypes.byref(scaler.c),
+                                     int(seed) & 0xFFFFFFFFFFFFFFFF, _current(stream)),
+          "zero_many_state_upload")
+
+
+def zero_many_state_download(many: ManyTensors, stream=None,
+                             scaler: Optional[LossScaler] = None) -> DeviceStepState:
+    """Read the device state back (waits); also refreshes `scaler` when given."""
+    t, skipped, last = ctypes.c_int64(0), ctypes.c_int64(0), ctypes.c_int32(0)
+    sc = _abi.zero_scaler_t()
+    check(lib.zero_many_state_download(many.handle, ctypes.byref(t), ctypes.byref(sc),
+                                       ctypes.byref(last), ctypes.byref(skipped),
+                                       _current(stream)), "zero_many_state_download")
+    if scaler is not None:
+        ctypes.memmove(ctypes.byref(scaler.c), ctypes.byref(sc), ctypes.sizeof(sc))
+    return DeviceStepState(int(t.value), int(skipped.value), int(last.value), float(sc.scale),
+                           int(sc.good_steps))
+
+
+def zero_many_device_scale(many: ManyTensors) -> int:
+    """Device address of the current loss scale (a double)."""
+    out = ctypes.c_void_p()
+    check(lib.zero_many_device_scale(many.handle, ctypes.byref(out)), "zero_many_device_scale")
+    return int(out.value)
+
+
+def zero_many_grad_norm(many: ManyTensors, sumsq, flag, stream=None) -> None:
+    """sumsq [1] (float64) = the sum of all squared gradients; flag [1] (int32) = 1 if any
+    is inf or NaN."""
+    torch = _torch()
+    _require(sumsq, "sumsq", 1, (torch.float64,))
+    _require(flag, "flag", 1, (torch.int32,))
+    check(lib.zero_many_grad_norm(many.handle, sumsq.data_ptr(), flag.data_ptr(),
+                                  _stream_handle(stream, sumsq.device)), "zero_many_grad_norm")
+
+
+def zero_many_adam_step(many: ManyTensors, hparams, flag=None, sumsq=None, max_norm: float = 0.0,
+                        norm_out=None, stream=None) -> None:
+    """One asynchronous, capturable step of every tensor.  hparams: an AdamHParams, or one per
+    group.  Skipped when flag [1] (int32) holds 1; clipped to max_norm (> 0) by sumsq;
+    norm_out [2] (float32) receives the gradient norm and the clip factor."""
+    torch = _torch()
+    groups = [hparams] if isinstance(hparams, AdamHParams) else list(hparams)
+    if flag is not None:
+        _require(flag, "flag", 1, (torch.int32,))
+    if sumsq is not None:
+        _require(sumsq, "sumsq", 1, (torch.float64,))
+    if norm_out is not None:
+        _require(norm_out, "norm_out", 2, (torch.float32,))
+    hp = (_abi.zero_adam_hparams_t * max(len(groups), 1))(*[g.to_c() for g in groups])
+    check(lib.zero_many_adam_step(many.handle, hp, len(groups), _ptr(flag), _ptr(sumsq),
+                                  float(max_norm), _ptr(norm_out), _current(stream)),
+          "zero_many_adam_step")
+
+
+def zero_many_state_values(many: ManyTensors, exp_avg=None, exp_avg_sq=None,
+                           stream=None) -> None:
+    """The moments as fp32 in the padded order (padded_numel elements, tensor i from
+    many.offsets()[i])."""
+    torch = _torch()
+    for name, t in (("exp_avg", exp_avg), ("exp_avg_sq", exp_avg_sq)):
+        if t is not None:
+            _require(t, name, many.padded_numel, (torch.float32,))
+    check(lib.zero_many_state_values(many.handle, _ptr(exp_avg), _ptr(exp_avg_sq),
+                                     _current(stream)), "zero_many_state_values")
 
 
 def zero_last_error() -> str:

@@ -72,6 +72,31 @@ class zero_scaler_t(ctypes.Structure):
                 ("dynamic", ctypes.c_int32), ("_pad", ctypes.c_int32)]
 
 
+class zero_preference_t(ctypes.Structure):
+    _fields_ = [("norm", ctypes.c_double), ("beta", ctypes.c_float),
+                ("label_smoothing", ctypes.c_float), ("kind", ctypes.c_int32),
+                ("average", ctypes.c_int32)]
+
+
+class zero_policy_t(ctypes.Structure):
+    _fields_ = [("norm", ctypes.c_double), ("clip_low", ctypes.c_float),
+                ("clip_high", ctypes.c_float), ("kl_coef", ctypes.c_float),
+                ("inv_temperature", ctypes.c_float)]
+
+
+class zero_many_info_t(ctypes.Structure):
+    _fields_ = [("total_numel", ctypes.c_int64), ("padded_numel", ctypes.c_int64),
+                ("state_bytes", ctypes.c_int64), ("n_tensors", ctypes.c_int32),
+                ("n_groups", ctypes.c_int32), ("state_bits", ctypes.c_int32),
+                ("_pad", ctypes.c_int32)]
+
+
+class zero_many_buffers_t(ctypes.Structure):
+    _fields_ = [(k, ctypes.c_void_p) for k in
+                ("grad", "master", "exp_avg", "exp_avg_sq", "exp_avg_scale", "exp_avg_sq_scale",
+                 "param")] + [("grad_dtype", ctypes.c_int32), ("param_dtype", ctypes.c_int32)]
+
+
 _VP = ctypes.c_void_p
 _I32 = ctypes.c_int32
 _I64 = ctypes.c_int64
@@ -116,6 +141,31 @@ SIGNATURES = {
     "zero_offload_destroy": (None, [_VP]),
     "zero_adam_scalars": (ctypes.c_int, [ctypes.POINTER(zero_adam_hparams_t), _I64, _I64,
                                          ctypes.c_double, _VP, _I32, _VP]),
+    "zero_token_logp": (ctypes.c_int, [_VP, _I32, _I64, _I64, _I64, _VP, ctypes.c_float, _VP, _VP,
+                                       _VP]),
+    "zero_token_logp_grad": (ctypes.c_int, [_VP, _I32, _I64, _I64, _I64, _VP, ctypes.c_float, _VP,
+                                            _VP, _VP, _I64, _VP]),
+    "zero_preference_loss": (ctypes.c_int, [_VP, _VP, _VP, _I64, _VP, _I64,
+                                            ctypes.POINTER(zero_preference_t), ctypes.c_double,
+                                            _VP, _VP, _VP, _VP, _VP, _VP]),
+    "zero_policy_loss": (ctypes.c_int, [_VP, _I32, _I64, _I64, _I64, _VP, _VP, _VP, _VP, _VP,
+                                        ctypes.POINTER(zero_policy_t), ctypes.c_double, _VP, _VP,
+                                        _VP, _VP, _VP, _I64, _VP]),
+    "zero_many_create": (ctypes.c_int, [_VP, _VP, _I32, _I32, _I32, ctypes.POINTER(_VP)]),
+    "zero_many_info": (ctypes.c_int, [_VP, ctypes.POINTER(zero_many_info_t)]),
+    "zero_many_offsets": (_I64, [_VP, _VP, _I64]),
+    "zero_many_destroy": (None, [_VP]),
+    "zero_many_bind": (ctypes.c_int, [_VP, ctypes.POINTER(zero_many_buffers_t), _VP]),
+    "zero_many_state_upload": (ctypes.c_int, [_VP, _I64, ctypes.POINTER(zero_scaler_t),
+                                              ctypes.c_uint64, _VP]),
+    "zero_many_state_download": (ctypes.c_int, [_VP, ctypes.POINTER(_I64),
+                                                ctypes.POINTER(zero_scaler_t),
+                                                ctypes.POINTER(_I32), ctypes.POINTER(_I64), _VP]),
+    "zero_many_device_scale": (ctypes.c_int, [_VP, ctypes.POINTER(_VP)]),
+    "zero_many_grad_norm": (ctypes.c_int, [_VP, _VP, _VP, _VP]),
+    "zero_many_adam_step": (ctypes.c_int, [_VP, ctypes.POINTER(zero_adam_hparams_t), _I32, _VP,
+                                           _VP, ctypes.c_double, _VP, _VP]),
+    "zero_many_state_values": (ctypes.c_int, [_VP, _VP, _VP, _VP]),
     "zero_last_error": (ctypes.c_char_p, []),
     "zero_plan_set_timing": (ctypes.c_int, [_VP, _I32]),
     "zero_plan_kernel_ms": (ctypes.c_int, [_VP, _I32, ctypes.POINTER(ctypes.c_float)]),

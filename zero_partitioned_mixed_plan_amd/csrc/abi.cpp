@@ -49,6 +49,21 @@ int check_hparams(const zero_adam_hparams_t* hp) {
     return ZERO_OK;
 }
 
+int check_scaler(const zero_scaler_t* sc) {
+    if (!(std::isfinite(sc->scale) && sc->scale > 0) ||
+        !(std::isfinite(sc->min_scale) && sc->min_scale > 0) ||
+        !(sc->backoff > 0 && sc->backoff <= 1) || !(std::isfinite(sc->growth) && sc->growth >= 1) ||
+        sc->window < 1 || sc->good_steps < 0) {
+        return fail(ZERO_EINVAL, "scaler fields out of range");
+    }
+    return ZERO_OK;
+}
+
+bool capturing(hipStream_t s) {
+    hipStreamCaptureStatus st = hipStreamCaptureStatusNone;
+    return hipStreamIsCapturing(s, &st) == hipSuccess && st != hipStreamCaptureStatusNone;
+}
+
 // Whether every real gradient of flat_grad went through the flatten (and so
 // through its overflow test) since the last step; if not, the step scans.
 bool flatten_covered(const zero_plan* p, const void* flat_grad, int32_t grad_dtype) {
@@ -197,11 +212,6 @@ int ensure_device(zero_plan* p, hipStream_t s, bool have_stream = true) {
 }
 
 // Event timing is skipped while the stream is being captured into a graph.
-bool capturing(hipStream_t s) {
-    hipStreamCaptureStatus st = hipStreamCaptureStatusNone;
-    return hipStreamIsCapturing(s, &st) == hipSuccess && st != hipStreamCaptureStatusNone;
-}
-
 int timer_start(zero_plan* p, Timer t, hipStream_t s) {
     if (!p->dev.timing || capturing(s)) return ZERO_OK;
     hipError_t e = hipEventRecord(p->dev.ev_start[t], s);
@@ -233,16 +243,6 @@ DeviceStep* device_step(zero_plan* p) {
 AdamScalars* device_scalars(zero_plan* p) {
     return reinterpret_cast<AdamScalars*>(reinterpret_cast<char*>(p->dev.d_flag) +
                                           kScalarsOffset);
-}
-
-int check_scaler(const zero_scaler_t* sc) {
-    if (!(std::isfinite(sc->scale) && sc->scale > 0) ||
-        !(std::isfinite(sc->min_scale) && sc->min_scale > 0) ||
-        !(sc->backoff > 0 && sc->backoff <= 1) || !(std::isfinite(sc->growth) && sc->growth >= 1) ||
-        sc->window < 1 || sc->good_steps < 0) {
-        return fail(ZERO_EINVAL, "scaler fields out of range");
-    }
-    return ZERO_OK;
 }
 
 // Host threads kept for zero_cpu_adam_step across calls (starting threads

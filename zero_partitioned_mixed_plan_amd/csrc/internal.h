@@ -29,6 +29,10 @@ int hip_fail(hipError_t e, const char* what);
 // ZERO_OK, or ZERO_EINVAL (with the message set) for hyperparameters out of
 // range: lr >= 0, 0 <= betas < 1, eps > 0, weight_decay >= 0, all finite.
 int check_hparams(const zero_adam_hparams_t* hp);
+// ZERO_OK, or ZERO_EINVAL (with the message set) for scaler fields out of range.
+int check_scaler(const zero_scaler_t* sc);
+// Whether the stream is being captured into a graph.
+bool capturing(hipStream_t s);
 
 // ---------------------------------------------------------------- plan
 struct Segment {

@@ -1,0 +1,82 @@
+// The many-tensor AdamW step: what its host side and its kernels share.
+#pragma once
+
+#include <vector>
+
+#include "internal.h"
+
+namespace zmi {
+
+constexpr int kManyBlock = ZERO_MANY_BLOCK;   // elements of one 8-bit scale
+constexpr int kManyChunk = 4 * kManyBlock;    // elements of one workgroup of the update
+
+// One tensor, as the kernels read it.
+struct ManyTensor {
+    uint64_t grad;  // 0: no gradient, the tensor is left alone
+    uint64_t master;
+    uint64_t m, v;
+    uint64_t m_scale, v_scale;
+    uint64_t param;  // 0: no half copy
+    int64_t numel;
+    int64_t chunk0;  // its first chunk
+    int64_t elem0;   // its first element in the padded order
+    int32_t group;
+    int32_t wide;    // bit 0: every array allows the wide path; bit 1: the gradient does
+};
+
+struct ManyScalars {
+    AdamScalars a;
+    int32_t adamw;
+    int32_t _pad;
+};
+
+// The handle's device block.
+struct ManyBlock {
+    DeviceStep st;
+    uint64_t seed;
+    int32_t skip;   // the step in flight changes nothing
+    uint32_t key;   // its random bits
+    ManyScalars sc[ZERO_MANY_MAX_GROUPS];
+};
+
+struct ManyHparams {
+    zero_adam_hparams_t g[ZERO_MANY_MAX_GROUPS];
+};
+
+constexpr int kNormParts = 2048;  // workgroups of the norm, at most
+
+struct ManyView {
+    const ManyTensor* tensors;
+    const uint32_t* chunk_tensor;  // the tensor of each chunk
+    int64_t n_chunks;
+    ManyBlock* block;
+    double* part;        // [kNormParts] sums of squares
+    int32_t* part_flag;  // [kNormParts]
+};
+
+hipError_t launch_many_norm(const ManyView& w, int grad_dtype, double* sumsq, int32_t* flag,
+                            hipStream_t s);
+hipError_t launch_many_prologue(const ManyView& w, const ManyHparams& hp, int n_groups,
+                                const int32_t* flag, const double* sumsq, double max_norm,
+                                float* norm_out, hipStream_t s);
+hipError_t launch_many_adam(const ManyView& w, int grad_dtype, int param_dtype, int state_bits,
+                            hipStream_t s);
+hipError_t launch_many_values(const ManyView& w, int state_bits, float* m, float* v,
+                              hipStream_t s);
+
+}  // namespace zmi
+
+struct zero_many {
+    std::vector<int64_t> numels;
+    std::vector<int32_t> groups;
+    std::vector<int64_t> offsets;  // padded first elements
+    int64_t total = 0, padded = 0, n_chunks = 0;
+    int32_t n_groups = 1, bits = 32;
+    // device side, made by the first device call
+    int device = -1;
+    bool ready = false, bound = false, full = false, state_ready = false;
+    int32_t grad_dtype = 0, param_dtype = 0;
+    char* d_mem = nullptr;  // block, partials, tensors, chunk table
+    char* h_mem = nullptr;  // pinned: block and tensors
+    zmi::ManyView view{};
+};
