@@ -8,131 +8,258 @@
 namespace zmi {
 namespace {
 
-constexpr int kRowThreads = 256;
+constexpr int kRowThreads = 256;  // of the per-pair and summing kernels
 constexpr float kLog2e = 1.44269504088896340736f;
 
-__device__ __forceinline__ float exp_fast(float x) { return __builtin_amdgcn_exp2f(x * kLog2e); }
+__device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
 
+// A vector of 16 bytes at any element's address: rows start wherever their
+// stride puts them.
 template <int DT>
-struct Word { typedef uint16_t T; };
+struct Elem {
+    typedef uint16_t T;
+    static constexpr int kPer = 8;
+    typedef uint32_t V __attribute__((ext_vector_type(4), aligned(2)));
+    static constexpr uint32_t kNegInf = DT == ZERO_BF16 ? 0xFF80FF80u : 0xFC00FC00u;
+};
 template <>
-struct Word<ZERO_F32> { typedef uint32_t T; };
+struct Elem<ZERO_F32> {
+    typedef uint32_t T;
+    static constexpr int kPer = 4;
+    typedef uint32_t V __attribute__((ext_vector_type(4), aligned(4)));
+    static constexpr uint32_t kNegInf = 0xFF800000u;
+};
 
 template <int DT>
-__device__ __forceinline__ typename Word<DT>::T from_f32(float x) {
+__device__ __forceinline__ typename Elem<DT>::T from_f32(float x) {
     if constexpr (DT == ZERO_F32) return __float_as_uint(x);
     else return f32_to_half<DT>(x);
 }
 
-template <int W>
-__device__ __forceinline__ float block_max(float x, float* lds) {
+// Element e of a vector.
+template <int DT>
+__device__ __forceinline__ float get(const u32x4& q, int e) {
+    if constexpr (DT == ZERO_F32) return __uint_as_float(q[e]);
+    if constexpr (DT == ZERO_BF16) {
+        return __uint_as_float((e & 1) ? (q[e >> 1] & 0xFFFF0000u) : (q[e >> 1] << 16));
+    }
+    return grad_to_f32<DT>((e & 1) ? (q[e >> 1] >> 16) : (q[e >> 1] & 0xFFFFu));
+}
+
+template <int DT>
+__device__ __forceinline__ u32x4 put(const float* d) {
+    u32x4 q;
+#pragma unroll
+    for (int w = 0; w < 4; ++w) {
+        if constexpr (DT == ZERO_F32) q[w] = __float_as_uint(d[w]);
+        else q[w] = uint32_t(f32_to_half<DT>(d[2 * w])) | (uint32_t(f32_to_half<DT>(d[2 * w + 1])) << 16);
+    }
+    return q;
+}
+
+// Vector k of a row; what lies behind the row's end is -inf.
+template <int DT>
+__device__ __forceinline__ u32x4 load_vec(const typename Elem<DT>::T* row, int vocab, int k) {
+    constexpr int per = Elem<DT>::kPer;
+    if (k * per + per <= vocab) {
+        return __builtin_nontemporal_load(reinterpret_cast<const typename Elem<DT>::V*>(row + k * per));
+    }
+    u32x4 q = {Elem<DT>::kNegInf, Elem<DT>::kNegInf, Elem<DT>::kNegInf, Elem<DT>::kNegInf};
+    for (int e = 0; k * per + e < vocab; ++e) {
+        const uint32_t x = row[k * per + e];
+        if constexpr (DT == ZERO_F32) q[e] = x;
+        else q[e >> 1] = (e & 1) ? ((q[e >> 1] & 0xFFFFu) | (x << 16)) : ((q[e >> 1] & 0xFFFF0000u) | x);
+    }
+    return q;
+}
+
+template <int DT>
+__device__ __forceinline__ void store_vec(typename Elem<DT>::T* row, int vocab, int k,
+                                          const u32x4& q) {
+    constexpr int per = Elem<DT>::kPer;
+    if (k * per + per <= vocab) {
+        __builtin_nontemporal_store(q, reinterpret_cast<typename Elem<DT>::V*>(row + k * per));
+        return;
+    }
+    for (int e = 0; k * per + e < vocab; ++e) {
+        if constexpr (DT == ZERO_F32) row[k * per + e] = q[e];
+        else row[k * per + e] = static_cast<uint16_t>((e & 1) ? (q[e >> 1] >> 16) : q[e >> 1]);
+    }
+}
+
+// Reductions over the T threads of a row (T = 64: one wave, no LDS; larger:
+// the whole workgroup).
+template <int T>
+__device__ __forceinline__ float row_max(float x, float* lds) {
 #pragma unroll
     for (int d = 32; d > 0; d >>= 1) x = fmaxf(x, __shfl_xor(x, d));
+    if (T == 64) return x;
     if ((threadIdx.x & 63) == 0) lds[threadIdx.x >> 6] = x;
     __syncthreads();
     x = lds[0];
 #pragma unroll
-    for (int w = 1; w < W; ++w) x = fmaxf(x, lds[w]);
+    for (int w = 1; w < T / 64; ++w) x = fmaxf(x, lds[w]);
+    return x;
+}
+
+template <int T>
+__device__ __forceinline__ double row_sum(double x, double* lds) {
+#pragma unroll
+    for (int d = 32; d > 0; d >>= 1) x += __shfl_xor(x, d);
+    if (T == 64) return x;
+    if ((threadIdx.x & 63) == 0) lds[threadIdx.x >> 6] = x;
+    __syncthreads();
+    x = lds[0];
+#pragma unroll
+    for (int w = 1; w < T / 64; ++w) x += lds[w];
     return x;
 }
 
 template <int W>
-__device__ __forceinline__ double block_sum(double x, double* lds) {
-#pragma unroll
-    for (int d = 32; d > 0; d >>= 1) x += __shfl_xor(x, d);
-    if ((threadIdx.x & 63) == 0) lds[threadIdx.x >> 6] = x;
-    __syncthreads();
-    x = lds[0];
-#pragma unroll
-    for (int w = 1; w < W; ++w) x += lds[w];
-    return x;
-}
+__device__ __forceinline__ double block_sum(double x, double* lds) { return row_sum<64 * W>(x, lds); }
 
-// Base (0 for a row of -inf alone) and sum of exp(x - base) of one row.
-template <int DT>
-__device__ __forceinline__ void row_stats(const typename Word<DT>::T* row, int64_t vocab,
-                                          float inv_t, float* base, double* sum) {
-    __shared__ float lmax[kRowThreads / 64];
-    __shared__ double lsum[kRowThreads / 64];
-    float m = -INFINITY;
-    for (int64_t j = threadIdx.x; j < vocab; j += kRowThreads) {
-        m = fmaxf(m, grad_to_f32<DT>(row[j]) * inv_t);
+// The largest finite value below: a base that an exponential's argument can
+// be taken from even where a row holds -inf alone (its sum is then 0).
+constexpr float kLowest = -3.402823466e38f;
+
+// Largest raw logit and the sum of exp((raw - largest) * inv_t) of one row,
+// read once: each thread keeps a running maximum and sum and rescales when
+// a group of vectors brings a larger value.
+template <int DT, int T>
+__device__ __forceinline__ void row_stats(const typename Elem<DT>::T* row, int vocab, float c,
+                                          int lane, float* lmax, double* lsum, float* top,
+                                          double* sum) {
+    constexpr int per = Elem<DT>::kPer, kGroup = 4;
+    const int nv = (vocab + per - 1) / per;
+    float m = kLowest, s = 0.f;
+    for (int k0 = lane; k0 < nv; k0 += T * kGroup) {
+        u32x4 q[kGroup];
+#pragma unroll
+        for (int i = 0; i < kGroup; ++i) {
+            const int k = k0 + i * T;
+            if (k < nv) q[i] = load_vec<DT>(row, vocab, k);
+            else q[i] = u32x4{Elem<DT>::kNegInf, Elem<DT>::kNegInf, Elem<DT>::kNegInf, Elem<DT>::kNegInf};
+        }
+        float g = m;
+#pragma unroll
+        for (int i = 0; i < kGroup; ++i) {
+#pragma unroll
+            for (int e = 0; e < per; ++e) g = fmaxf(g, get<DT>(q[i], e));
+        }
+        s *= exp2_fast((m - g) * c);
+        m = g;
+#pragma unroll
+        for (int i = 0; i < kGroup; ++i) {
+#pragma unroll
+            for (int e = 0; e < per; ++e) s += exp2_fast((get<DT>(q[i], e) - m) * c);
+        }
     }
-    m = block_max<kRowThreads / 64>(m, lmax);
-    if (m == -INFINITY) m = 0.f;
-    float s = 0.f;
-    for (int64_t j = threadIdx.x; j < vocab; j += kRowThreads) {
-        s += exp_fast(grad_to_f32<DT>(row[j]) * inv_t - m);
-    }
-    *base = m;
-    *sum = block_sum<kRowThreads / 64>(s, lsum);
+    *top = row_max<T>(m, lmax);
+    *sum = row_sum<T>(static_cast<double>(s * exp2_fast((m - *top) * c)), lsum);
 }
 
 // log-probability of the label, in fp64: -inf when the row holds nothing,
 // NaN for a label outside the vocabulary.
 template <int DT>
-__device__ __forceinline__ double label_logp(const typename Word<DT>::T* row, int64_t label,
-                                             int64_t vocab, float inv_t, double lse) {
+__device__ __forceinline__ double label_logp(const typename Elem<DT>::T* row, int64_t label,
+                                             int vocab, float inv_t, double lse) {
     if (label >= vocab) return NAN;
     if (lse == -INFINITY) return -INFINITY;
-    return static_cast<double>(grad_to_f32<DT>(row[label]) * inv_t) - lse;
+    return static_cast<double>(grad_to_f32<DT>(row[label])) * static_cast<double>(inv_t) - lse;
 }
 
-template <int DT>
-__global__ void __launch_bounds__(kRowThreads)
-logp_kernel(const typename Word<DT>::T* __restrict__ logits, int64_t rows, int64_t vocab,
+// Rows a workgroup of the row kernels takes, and its threads.
+template <int T>
+constexpr int rows_per_group() { return T == 64 ? 4 : 1; }
+
+template <int DT, int T>
+__global__ void __launch_bounds__(T * rows_per_group<T>())
+logp_kernel(const typename Elem<DT>::T* __restrict__ logits, int64_t rows, int vocab,
             int64_t stride, const int64_t* __restrict__ labels, float inv_t,
             float* __restrict__ logp, float* __restrict__ lse) {
-    const int64_t r = block_id();
+    __shared__ float lmax[T / 64];
+    __shared__ double lsum[T / 64];
+    const int lane = static_cast<int>(threadIdx.x) % T;
+    const int64_t r = block_id() * rows_per_group<T>() + threadIdx.x / T;
     if (r >= rows) return;
     const int64_t label = labels[r];
     if (label < 0) {
-        if (threadIdx.x == 0) {
+        if (lane == 0) {
             logp[r] = 0.f;
             if (lse != nullptr) lse[r] = 0.f;
         }
         return;
     }
     const auto* row = logits + r * stride;
-    float base;
+    float top;
     double sum;
-    row_stats<DT>(row, vocab, inv_t, &base, &sum);
-    if (threadIdx.x == 0) {
-        const double l = static_cast<double>(base) + log(sum);
+    row_stats<DT, T>(row, vocab, inv_t * kLog2e, lane, lmax, lsum, &top, &sum);
+    if (lane == 0) {
+        const double l = static_cast<double>(top) * static_cast<double>(inv_t) + log(sum);
         logp[r] = static_cast<float>(label_logp<DT>(row, label, vocab, inv_t, l));
         if (lse != nullptr) lse[r] = static_cast<float>(l);
     }
 }
 
-// One row of gradient: g ([j == label] - exp(x - lse)), g with the
-// temperature in it; zeros when g is 0 or the row holds nothing.
-template <int DT>
-__device__ __forceinline__ void write_row(const typename Word<DT>::T* row,
-                                          typename Word<DT>::T* out, int64_t vocab, int64_t label,
-                                          float inv_t, float lse, float g) {
-    const bool zero = g == 0.f || lse == -INFINITY;
-    for (int64_t j = threadIdx.x; j < vocab; j += kRowThreads) {
-        float d = 0.f;
-        if (!zero) {
-            const float p = exp_fast(grad_to_f32<DT>(row[j]) * inv_t - lse);
-            d = g * ((j == label ? 1.f : 0.f) - p);
-        }
-        out[j] = from_f32<DT>(d);
-    }
+// Zeros over one row.
+template <int DT, int T>
+__device__ __forceinline__ void zero_row(typename Elem<DT>::T* out, int vocab, int lane) {
+    constexpr int per = Elem<DT>::kPer;
+    const int nv = (vocab + per - 1) / per;
+    for (int k = lane; k < nv; k += T) store_vec<DT>(out, vocab, k, u32x4{0, 0, 0, 0});
 }
 
+// One vector of gradient: -g exp2((raw - base) c - shift).
 template <int DT>
-__global__ void __launch_bounds__(kRowThreads)
-logp_grad_kernel(const typename Word<DT>::T* logits, int64_t rows, int64_t vocab, int64_t stride,
+__device__ __forceinline__ u32x4 grad_vec(const u32x4& q, float base, float c, float shift,
+                                          float g) {
+    float d[Elem<DT>::kPer];
+#pragma unroll
+    for (int e = 0; e < Elem<DT>::kPer; ++e) {
+        d[e] = -g * exp2_fast((get<DT>(q, e) - base) * c - shift);
+    }
+    return put<DT>(d);
+}
+
+template <int DT, int T>
+__global__ void __launch_bounds__(T * rows_per_group<T>())
+logp_grad_kernel(const typename Elem<DT>::T* logits, int64_t rows, int vocab, int64_t stride,
                  const int64_t* __restrict__ labels, float inv_t, const float* __restrict__ lse,
-                 const float* __restrict__ dlogp, typename Word<DT>::T* dlogits,
+                 const float* __restrict__ dlogp, typename Elem<DT>::T* dlogits,
                  int64_t out_stride) {
-    const int64_t r = block_id();
+    constexpr int per = Elem<DT>::kPer, kGroup = 4;
+    const int lane = static_cast<int>(threadIdx.x) % T;
+    const int64_t r = block_id() * rows_per_group<T>() + threadIdx.x / T;
     if (r >= rows) return;
     const int64_t label = labels[r];
     const float g = label < 0 ? 0.f : dlogp[r] * inv_t;
-    write_row<DT>(logits + r * stride, dlogits + r * out_stride, vocab, label, inv_t,
-                  g == 0.f ? 0.f : lse[r], g);
+    const float l = g == 0.f ? 0.f : lse[r];
+    const auto* row = logits + r * stride;
+    auto* out = dlogits + r * out_stride;
+    if (g == 0.f || l == -INFINITY) return zero_row<DT, T>(out, vocab, lane);
+    const float c = inv_t * kLog2e, shift = l * kLog2e;
+    const int nv = (vocab + per - 1) / per;
+    const int mine = label < vocab ? static_cast<int>(label) / per : -1;
+    for (int k0 = lane; k0 < nv; k0 += T * kGroup) {
+        u32x4 q[kGroup];
+#pragma unroll
+        for (int i = 0; i < kGroup; ++i) {
+            const int k = k0 + i * T;
+            if (k < nv) q[i] = load_vec<DT>(row, vocab, k);
+        }
+#pragma unroll
+        for (int i = 0; i < kGroup; ++i) {
+            const int k = k0 + i * T;
+            if (k < nv) store_vec<DT>(out, vocab, k, grad_vec<DT>(q[i], 0.f, c, shift, g));
+            if (k == mine) {
+                const int e = static_cast<int>(label) % per;
+                float x = 0.f;
+#pragma unroll
+                for (int j = 0; j < per; ++j) x = j == e ? get<DT>(q[i], j) : x;
+                out[label] = from_f32<DT>(g * (1.f - exp2_fast(x * c - shift)));
+            }
+        }
+    }
 }
 
 // ------------------------------------------------------------ preference
@@ -235,50 +362,130 @@ __device__ __forceinline__ double policy_token(double logp, float old, const flo
     return (clipped ? 0.0 : -kept) + static_cast<double>(cfg.kl_coef) * dkl;
 }
 
+// What every thread of a row needs for its gradient.
+struct RowGrad {
+    float base, c, shift, g, at_label;
+};
+
+// The terms of row r from its statistics; the row's gradient is
+// -g exp2((raw - base) c - shift), and at_label at the label.
 template <int DT>
-__global__ void __launch_bounds__(kRowThreads)
-policy_kernel(const typename Word<DT>::T* logits, int64_t rows, int64_t vocab, int64_t stride,
+__device__ __forceinline__ RowGrad policy_row(const typename Elem<DT>::T* row, int64_t r,
+                                              int64_t label, int vocab, float top, double sum,
+                                              const float* old, const float* ref, const float* adv,
+                                              const float* weight, const zero_policy_t& cfg,
+                                              double scale, float* logp, PolicyTerms* terms) {
+    const double lsum = log(sum);
+    const double lse = static_cast<double>(top) * static_cast<double>(cfg.inv_temperature) + lsum;
+    const double lp = label_logp<DT>(row, label, vocab, cfg.inv_temperature, lse);
+    const float w = weight != nullptr ? weight[r] : 1.f;
+    PolicyTerms t{0.f, 0.f, 0.f, 0.f};
+    float g = 0.f;
+    if (w != 0.f) {
+        g = static_cast<float>(
+            policy_token(lp, old[r], ref != nullptr ? ref + r : nullptr, adv[r], w, cfg, &t) *
+            (scale * cfg.norm * static_cast<double>(w)));
+    }
+    logp[r] = static_cast<float>(lp);
+    terms[r] = t;
+    RowGrad o;
+    o.base = top;
+    o.c = cfg.inv_temperature * kLog2e;
+    o.shift = static_cast<float>(lsum * 1.4426950408889634074);
+    o.g = lse == -INFINITY ? 0.f : g * cfg.inv_temperature;
+    o.at_label = o.g * static_cast<float>(-expm1(lp));
+    return o;
+}
+
+// Writes a row of gradient from a source of its vectors.
+template <int DT, int T>
+__device__ __forceinline__ void patch_label(typename Elem<DT>::T* out, int64_t label, int vocab,
+                                            int k, float at_label) {
+    if (label < vocab && k == static_cast<int>(label) / Elem<DT>::kPer) {
+        out[label] = from_f32<DT>(at_label);
+    }
+}
+
+// VPT > 0: the row stays in registers, VPT vectors a thread, between its
+// statistics and its gradient.  VPT = 0: it is read twice.
+template <int DT, int T, int VPT>
+__global__ void __launch_bounds__(T * rows_per_group<T>())
+policy_kernel(const typename Elem<DT>::T* logits, int64_t rows, int vocab, int64_t stride,
               const int64_t* __restrict__ labels, const float* __restrict__ old,
               const float* __restrict__ ref, const float* __restrict__ adv,
               const float* __restrict__ weight, const zero_policy_t cfg, double scale_host,
               const double* __restrict__ scale_dev, float* __restrict__ logp,
-              PolicyTerms* __restrict__ terms, typename Word<DT>::T* dlogits, int64_t out_stride) {
-    __shared__ float coef[2];
-    const int64_t r = block_id();
+              PolicyTerms* __restrict__ terms, typename Elem<DT>::T* dlogits, int64_t out_stride) {
+    __shared__ float lmax[T / 64];
+    __shared__ double lsum[T / 64];
+    __shared__ RowGrad share[rows_per_group<T>()];
+    constexpr int per = Elem<DT>::kPer;
+    const int lane = static_cast<int>(threadIdx.x) % T;
+    const int64_t r = block_id() * rows_per_group<T>() + threadIdx.x / T;
     if (r >= rows) return;
     const int64_t label = labels[r];
     const auto* row = logits + r * stride;
     auto* out = dlogits + r * out_stride;
     if (label < 0) {
-        if (threadIdx.x == 0) {
+        if (lane == 0) {
             logp[r] = 0.f;
             terms[r] = PolicyTerms{0.f, 0.f, 0.f, 0.f};
         }
-        write_row<DT>(row, out, vocab, label, 1.f, 0.f, 0.f);
-        return;
+        return zero_row<DT, T>(out, vocab, lane);
     }
-    float base;
+    const int nv = (vocab + per - 1) / per;
+    const float c = cfg.inv_temperature * kLog2e;
+    float top;
     double sum;
-    row_stats<DT>(row, vocab, cfg.inv_temperature, &base, &sum);
-    if (threadIdx.x == 0) {
-        const double lse = static_cast<double>(base) + log(sum);
-        const double lp = label_logp<DT>(row, label, vocab, cfg.inv_temperature, lse);
-        const float w = weight != nullptr ? weight[r] : 1.f;
-        logp[r] = static_cast<float>(lp);
-        PolicyTerms t{0.f, 0.f, 0.f, 0.f};
-        float g = 0.f;
-        if (w != 0.f) {
-            const double scale = scale_dev != nullptr ? *scale_dev : scale_host;
-            g = static_cast<float>(
-                policy_token(lp, old[r], ref != nullptr ? ref + r : nullptr, adv[r], w, cfg, &t) *
-                (scale * cfg.norm * static_cast<double>(w)));
+    u32x4 q[VPT > 0 ? VPT : 1];
+    if (VPT > 0) {
+#pragma unroll
+        for (int i = 0; i < VPT; ++i) {
+            const int k = lane + i * T;
+            if (k < nv) q[i] = load_vec<DT>(row, vocab, k);
+            else q[i] = u32x4{Elem<DT>::kNegInf, Elem<DT>::kNegInf, Elem<DT>::kNegInf, Elem<DT>::kNegInf};
         }
-        terms[r] = t;
-        coef[0] = static_cast<float>(lse);
-        coef[1] = g * cfg.inv_temperature;
+        float m = kLowest, s = 0.f;
+#pragma unroll
+        for (int i = 0; i < VPT; ++i) {
+#pragma unroll
+            for (int e = 0; e < per; ++e) m = fmaxf(m, get<DT>(q[i], e));
+        }
+        top = row_max<T>(m, lmax);
+#pragma unroll
+        for (int i = 0; i < VPT; ++i) {
+#pragma unroll
+            for (int e = 0; e < per; ++e) s += exp2_fast((get<DT>(q[i], e) - top) * c);
+        }
+        sum = row_sum<T>(static_cast<double>(s), lsum);
+    } else {
+        row_stats<DT, T>(row, vocab, c, lane, lmax, lsum, &top, &sum);
     }
-    __syncthreads();  // also: in place, the label's logit is read before any write
-    write_row<DT>(row, out, vocab, label, cfg.inv_temperature, coef[0], coef[1]);
+    const int slot = T == 64 ? static_cast<int>(threadIdx.x / T) : 0;
+    if (lane == 0) {
+        share[slot] = policy_row<DT>(row, r, label, vocab, top, sum, old, ref, adv, weight, cfg,
+                                     scale_dev != nullptr ? *scale_dev : scale_host, logp, terms);
+    }
+    // T = 64: the row's own wave wrote its slot
+    if (T > 64) __syncthreads();
+    else __builtin_amdgcn_wave_barrier();
+    const RowGrad o = share[slot];
+    if (o.g == 0.f) return zero_row<DT, T>(out, vocab, lane);
+    if (VPT > 0) {
+#pragma unroll
+        for (int i = 0; i < VPT; ++i) {
+            const int k = lane + i * T;
+            if (k >= nv) break;
+            store_vec<DT>(out, vocab, k, grad_vec<DT>(q[i], o.base, o.c, o.shift, o.g));
+            patch_label<DT, T>(out, label, vocab, k, o.at_label);
+        }
+    } else {
+        for (int k = lane; k < nv; k += T) {
+            const u32x4 x = load_vec<DT>(row, vocab, k);
+            store_vec<DT>(out, vocab, k, grad_vec<DT>(x, o.base, o.c, o.shift, o.g));
+            patch_label<DT, T>(out, label, vocab, k, o.at_label);
+        }
+    }
 }
 
 // One workgroup: the four sums of the batch.
@@ -373,13 +580,50 @@ int launched(const char* what) {
     return e == hipSuccess ? ZERO_OK : hip_fail(e, what);
 }
 
+template <int N>
+using Const = std::integral_constant<int, N>;
+
 // Calls f with the dtype as a compile-time constant.
 template <typename F>
 void with_dtype(int32_t dtype, F f) {
-    if (dtype == ZERO_F16) f(std::integral_constant<int, ZERO_F16>());
-    else if (dtype == ZERO_BF16) f(std::integral_constant<int, ZERO_BF16>());
-    else f(std::integral_constant<int, ZERO_F32>());
+    if (dtype == ZERO_F16) f(Const<ZERO_F16>());
+    else if (dtype == ZERO_BF16) f(Const<ZERO_BF16>());
+    else f(Const<ZERO_F32>());
 }
+
+// Calls f with the threads that take a row of nv vectors.
+template <typename F>
+void with_threads(int64_t nv, int64_t rows, F f) {
+    if (nv <= 64 * 8 && rows >= 2048) f(Const<64>());
+    else if (nv <= 256 * 16) f(Const<256>());
+    else if (nv <= 512 * 16) f(Const<512>());
+    else f(Const<1024>());
+}
+
+// The same for a kernel that keeps the row in registers: threads and
+// vectors per thread (0: the row does not fit).
+template <typename F>
+void with_row_shape(int64_t nv, int64_t rows, F f) {
+    if (nv <= 64 * 8 && rows >= 2048) f(Const<64>(), Const<8>());
+    else if (nv <= 256 * 4) f(Const<256>(), Const<4>());
+    else if (nv <= 256 * 8) f(Const<256>(), Const<8>());
+    else if (nv <= 256 * 16) f(Const<256>(), Const<16>());
+    else if (nv <= 512 * 16) f(Const<512>(), Const<16>());
+    else if (nv <= 1024 * 16) f(Const<1024>(), Const<16>());
+    else f(Const<1024>(), Const<0>());
+}
+
+int64_t vectors(int32_t dtype, int64_t vocab) {
+    const int64_t per = dtype == ZERO_F32 ? 4 : 8;
+    return (vocab + per - 1) / per;
+}
+
+template <int T>
+dim3 row_grid(int64_t rows) {
+    return grid_2d((rows + rows_per_group<T>() - 1) / rows_per_group<T>());
+}
+template <int T>
+dim3 row_block() { return dim3(T * rows_per_group<T>()); }
 
 }  // namespace
 }  // namespace zmi
@@ -399,9 +643,13 @@ int zero_token_logp(const void* logits, int32_t dtype, int64_t rows, int64_t voc
     hipStream_t s = static_cast<hipStream_t>(stream);
     with_dtype(dtype, [&](auto dt) {
         constexpr int DT = decltype(dt)::value;
-        hipLaunchKernelGGL((logp_kernel<DT>), grid_2d(rows), dim3(kRowThreads), 0, s,
-                           static_cast<const typename Word<DT>::T*>(logits), rows, vocab,
-                           row_stride, labels, inv_temperature, logp, lse);
+        with_threads(vectors(dtype, vocab), rows, [&](auto threads) {
+            constexpr int T = decltype(threads)::value;
+            hipLaunchKernelGGL((logp_kernel<DT, T>), row_grid<T>(rows), row_block<T>(), 0, s,
+                               static_cast<const typename Elem<DT>::T*>(logits), rows,
+                               static_cast<int>(vocab), row_stride, labels, inv_temperature, logp,
+                               lse);
+        });
     });
     return launched("log-probability launch");
 }
@@ -419,10 +667,13 @@ int zero_token_logp_grad(const void* logits, int32_t dtype, int64_t rows, int64_
     hipStream_t s = static_cast<hipStream_t>(stream);
     with_dtype(dtype, [&](auto dt) {
         constexpr int DT = decltype(dt)::value;
-        hipLaunchKernelGGL((logp_grad_kernel<DT>), grid_2d(rows), dim3(kRowThreads), 0, s,
-                           static_cast<const typename Word<DT>::T*>(logits), rows, vocab,
-                           row_stride, labels, inv_temperature, lse, dlogp,
-                           static_cast<typename Word<DT>::T*>(dlogits), dlogits_stride);
+        with_threads(vectors(dtype, vocab), rows, [&](auto threads) {
+            constexpr int T = decltype(threads)::value;
+            hipLaunchKernelGGL((logp_grad_kernel<DT, T>), row_grid<T>(rows), row_block<T>(), 0, s,
+                               static_cast<const typename Elem<DT>::T*>(logits), rows,
+                               static_cast<int>(vocab), row_stride, labels, inv_temperature, lse,
+                               dlogp, static_cast<typename Elem<DT>::T*>(dlogits), dlogits_stride);
+        });
     });
     return launched("log-probability gradient launch");
 }
@@ -493,11 +744,14 @@ int zero_policy_loss(const void* logits, int32_t dtype, int64_t rows, int64_t vo
     if (rows > 0) {
         with_dtype(dtype, [&](auto dt) {
             constexpr int DT = decltype(dt)::value;
-            hipLaunchKernelGGL((policy_kernel<DT>), grid_2d(rows), dim3(kRowThreads), 0, s,
-                               static_cast<const typename Word<DT>::T*>(logits), rows, vocab,
-                               row_stride, labels, old_logp, ref_logp, advantage, weight, *cfg,
-                               loss_scale, loss_scale_dev, logp, t,
-                               static_cast<typename Word<DT>::T*>(dlogits), dlogits_stride);
+            with_row_shape(vectors(dtype, vocab), rows, [&](auto threads, auto vecs) {
+                constexpr int T = decltype(threads)::value, V = decltype(vecs)::value;
+                hipLaunchKernelGGL((policy_kernel<DT, T, V>), row_grid<T>(rows), row_block<T>(), 0,
+                                   s, static_cast<const typename Elem<DT>::T*>(logits), rows,
+                                   static_cast<int>(vocab), row_stride, labels, old_logp, ref_logp,
+                                   advantage, weight, *cfg, loss_scale, loss_scale_dev, logp, t,
+                                   static_cast<typename Elem<DT>::T*>(dlogits), dlogits_stride);
+            });
         });
     }
     hipLaunchKernelGGL(policy_sum_kernel, dim3(1), dim3(kRowThreads), 0, s, t, rows, cfg->norm,
