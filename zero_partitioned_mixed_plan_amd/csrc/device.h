@@ -48,6 +48,48 @@ __device__ __forceinline__ uint16_t f32_to_half(float x) {
     return __builtin_bit_cast(uint16_t, static_cast<_Float16>(x));
 }
 
+// Reductions over a wave's 64 lanes on the cross-lane data path (DPP: shifts
+// within rows of 16 lanes, then two broadcasts across them), a few cycles a
+// step where a permute through LDS takes tens.  The result is uniform.
+template <int CTRL, int ROWS>
+__device__ __forceinline__ int dpp(int x, int identity) {
+    return __builtin_amdgcn_update_dpp(identity, x, CTRL, ROWS, 0xF, false);
+}
+
+template <int CTRL, int ROWS>
+__device__ __forceinline__ float dpp_max(float x, float identity) {
+    return fmaxf(x, __int_as_float(dpp<CTRL, ROWS>(__float_as_int(x), __float_as_int(identity))));
+}
+
+// The largest value (NaNs aside).
+__device__ __forceinline__ float wave_max(float x, float identity = -__builtin_inff()) {
+    x = dpp_max<0x111, 0xF>(x, identity);
+    x = dpp_max<0x112, 0xF>(x, identity);
+    x = dpp_max<0x114, 0xF>(x, identity);
+    x = dpp_max<0x118, 0xF>(x, identity);
+    x = dpp_max<0x142, 0xA>(x, identity);
+    x = dpp_max<0x143, 0xC>(x, identity);
+    return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(x), 63));
+}
+
+template <int CTRL, int ROWS>
+__device__ __forceinline__ double dpp_add(double x) {
+    const int lo = dpp<CTRL, ROWS>(__double2loint(x), 0);
+    const int hi = dpp<CTRL, ROWS>(__double2hiint(x), 0);
+    return x + __hiloint2double(hi, lo);
+}
+
+__device__ __forceinline__ double wave_sum(double x) {
+    x = dpp_add<0x111, 0xF>(x);
+    x = dpp_add<0x112, 0xF>(x);
+    x = dpp_add<0x114, 0xF>(x);
+    x = dpp_add<0x118, 0xF>(x);
+    x = dpp_add<0x142, 0xA>(x);
+    x = dpp_add<0x143, 0xC>(x);
+    return __hiloint2double(__builtin_amdgcn_readlane(__double2hiint(x), 63),
+                            __builtin_amdgcn_readlane(__double2loint(x), 63));
+}
+
 // One element of the update, fp32, one rounding per operation.
 template <bool ADAMW>
 __device__ __forceinline__ void adam_elem(float g, float& p, float& m, float& v,
