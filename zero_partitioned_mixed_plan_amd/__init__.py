@@ -113,6 +113,12 @@ def _grad_dtypes():
 def _stream_handle(stream, device) -> Optional[int]:
     torch = _torch()
     if stream is None:
+        # the handle alone, where torch offers it: building the Stream object
+        # takes 2 us of a call whose launch takes 3
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        if raw is not None:
+            index = device.index
+            return raw(torch.cuda.current_device() if index is None else index)
         stream = torch.cuda.current_stream(device)
     return stream.cuda_stream
 
@@ -672,9 +678,11 @@ def _matrix(t, name: str, dtypes):
     if t.dtype not in dtypes:
         raise TypeError(f"{name} has dtype {t.dtype}, expected one of {dtypes}")
     rows, vocab = t.shape
-    if vocab > 1 and t.stride(1) != 1:
+    stride, unit = t.stride()
+    if vocab > 1 and unit != 1:
         raise ValueError(f"{name} must have unit stride along the vocabulary")
-    stride = t.stride(0) if rows > 1 else max(vocab, 1)
+    if rows <= 1:
+        stride = max(vocab, 1)
     if stride < vocab:
         raise ValueError(f"{name} has overlapping rows")
     return rows, vocab, stride
@@ -687,10 +695,17 @@ def _logits_and_labels(logits, labels):
     return rows, vocab, stride
 
 
-def _floats(rows: int, **tensors) -> None:
+def _f32(t, name: str, min_numel: int) -> int:
+    """The address of a contiguous float32 device tensor of at least min_numel elements."""
     torch = _torch()
-    for name, t in tensors.items():
-        _require(t, name, rows, (torch.float32,))
+    if not (isinstance(t, torch.Tensor) and t.dtype == torch.float32 and t.is_cuda and
+            t.numel() >= min_numel and t.is_contiguous()):
+        _require(t, name, min_numel, (torch.float32,))
+    return t.data_ptr()
+
+
+def _f32_or_none(t, name: str, min_numel: int) -> Optional[int]:
+    return None if t is None else _f32(t, name, min_numel)
 
 
 def _dlogits(dlogits, logits):
@@ -709,12 +724,10 @@ def zero_token_logp(logits, labels, logp, lse=None, inv_temperature: float = 1.0
     """logp[r] = the log-probability of labels[r] (int64; negative: masked, 0) under
     softmax(logits[r] * inv_temperature); lse[r] = the row's log-sum-exp."""
     rows, vocab, stride = _logits_and_labels(logits, labels)
-    _floats(rows, logp=logp)
-    if lse is not None:
-        _floats(rows, lse=lse)
     check(lib.zero_token_logp(logits.data_ptr(), _dtype_code(logits), rows, vocab, stride,
-                              labels.data_ptr(), float(inv_temperature), logp.data_ptr(),
-                              _ptr(lse), _stream_handle(stream, logits.device)),
+                              labels.data_ptr(), float(inv_temperature),
+                              _f32(logp, "logp", rows), _f32_or_none(lse, "lse", rows),
+                              _stream_handle(stream, logits.device)),
           "zero_token_logp")
 
 
@@ -723,10 +736,10 @@ def zero_token_logp_grad(logits, labels, lse, dlogp, dlogits, inv_temperature: f
     """dlogits = the gradient of sum(dlogp * logp) to the logits, in their dtype; dlogits may
     be the logits tensor itself."""
     rows, vocab, stride = _logits_and_labels(logits, labels)
-    _floats(rows, lse=lse, dlogp=dlogp)
     check(lib.zero_token_logp_grad(logits.data_ptr(), _dtype_code(logits), rows, vocab, stride,
-                                   labels.data_ptr(), float(inv_temperature), lse.data_ptr(),
-                                   dlogp.data_ptr(), dlogits.data_ptr(), _dlogits(dlogits, logits),
+                                   labels.data_ptr(), float(inv_temperature),
+                                   _f32(lse, "lse", rows), _f32(dlogp, "dlogp", rows),
+                                   dlogits.data_ptr(), _dlogits(dlogits, logits),
                                    _stream_handle(stream, logits.device)),
           "zero_token_logp_grad")
 
@@ -753,23 +766,19 @@ def zero_preference_loss(logp, ref_logp, seq_offsets, loss, pair_loss, rewards, 
     if seq_offsets.numel() % 2 != 1:
         raise ValueError("seq_offsets must hold 2 * pairs + 1 offsets")
     pairs = seq_offsets.numel() // 2
-    _floats(0, logp=logp)
+    logp_ptr = _f32(logp, "logp", 0)
     rows = logp.numel()
-    _floats(rows, dlogp=dlogp)
-    _floats(1, loss=loss)
-    _floats(pairs, pair_loss=pair_loss)
-    _floats(2 * pairs, rewards=rewards)
-    if ref_logp is not None:
-        _floats(rows, ref_logp=ref_logp)
     if labels is not None:
         _require(labels, "labels", rows, (torch.int64,))
     cfg = _abi.zero_preference_t(1.0 / max(pairs, 1) if norm is None else float(norm),
                                  float(beta), float(label_smoothing), _PREFERENCE_KINDS[kind],
                                  1 if average else 0)
-    check(lib.zero_preference_loss(logp.data_ptr(), _ptr(ref_logp), _ptr(labels), rows,
-                                   seq_offsets.data_ptr(), pairs, ctypes.byref(cfg),
-                                   float(loss_scale), loss_scale_dev, loss.data_ptr(),
-                                   pair_loss.data_ptr(), rewards.data_ptr(), dlogp.data_ptr(),
+    check(lib.zero_preference_loss(logp_ptr, _f32_or_none(ref_logp, "ref_logp", rows),
+                                   _ptr(labels), rows, seq_offsets.data_ptr(), pairs,
+                                   ctypes.byref(cfg), float(loss_scale), loss_scale_dev,
+                                   _f32(loss, "loss", 1), _f32(pair_loss, "pair_loss", pairs),
+                                   _f32(rewards, "rewards", 2 * pairs),
+                                   _f32(dlogp, "dlogp", rows),
                                    _stream_handle(stream, logp.device)), "zero_preference_loss")
 
 
@@ -784,21 +793,16 @@ def zero_policy_loss(logits, labels, old_logp, advantage, dlogits, logp, terms, 
     [rows, 4] = each token's policy part, KL, clipped, weight; dlogits may be the logits
     tensor itself.  loss_scale_dev as in zero_preference_loss."""
     rows, vocab, stride = _logits_and_labels(logits, labels)
-    _floats(rows, old_logp=old_logp, advantage=advantage, logp=logp)
-    _floats(4 * rows, terms=terms)
-    _floats(4, loss=loss)
-    if ref_logp is not None:
-        _floats(rows, ref_logp=ref_logp)
-    if weight is not None:
-        _floats(rows, weight=weight)
     cfg = _abi.zero_policy_t(float(norm), float(clip_low), float(clip_high), float(kl_coef),
                              float(inv_temperature))
     check(lib.zero_policy_loss(logits.data_ptr(), _dtype_code(logits), rows, vocab, stride,
-                               labels.data_ptr(), old_logp.data_ptr(), _ptr(ref_logp),
-                               advantage.data_ptr(), _ptr(weight), ctypes.byref(cfg),
-                               float(loss_scale), loss_scale_dev, logp.data_ptr(),
-                               terms.data_ptr(), loss.data_ptr(), dlogits.data_ptr(),
-                               _dlogits(dlogits, logits), _stream_handle(stream, logits.device)),
+                               labels.data_ptr(), _f32(old_logp, "old_logp", rows),
+                               _f32_or_none(ref_logp, "ref_logp", rows),
+                               _f32(advantage, "advantage", rows),
+                               _f32_or_none(weight, "weight", rows), ctypes.byref(cfg),
+                               float(loss_scale), loss_scale_dev, _f32(logp, "logp", rows),
+                               _f32(terms, "terms", 4 * rows), _f32(loss, "loss", 4),
+                               dlogits.data_ptr(), _dlogits(dlogits, logits), _stream_handle(stream, logits.device)),
           "zero_policy_loss")
 
 
