@@ -98,7 +98,6 @@ int fill_tensor(const zero_many* w, const zero_many_buffers_t* b, size_t i, int6
     const uint64_t gsize = b->grad_dtype == ZERO_F32 ? 4 : 2;
     uint64_t mis = t->grad % (4 * gsize);
     bool off = t->grad % gsize != 0;
-    t->wide = t->grad % 16 == 0 ? 2 : 0;
     if (full) {
         t->master = address(b->master[i]);
         t->m = address(b->exp_avg[i]);
@@ -134,7 +133,7 @@ int fill_tensor(const zero_many* w, const zero_many_buffers_t* b, size_t i, int6
         return fail(ZERO_EALIGN, "tensor " + std::to_string(i) +
                                      ": a pointer is not aligned to its element");
     }
-    if (mis == 0) t->wide |= 1;
+    t->wide = mis == 0;
     return ZERO_OK;
 }
 

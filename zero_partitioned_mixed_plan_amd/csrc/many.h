@@ -8,7 +8,9 @@
 namespace zmi {
 
 constexpr int kManyBlock = ZERO_MANY_BLOCK;   // elements of one 8-bit scale
-constexpr int kManyChunk = 4 * kManyBlock;    // elements of one workgroup of the update
+constexpr int kManyBlocks = 4;                // blocks of one wave of the update
+constexpr int kManyWaves = 4;                 // waves of one workgroup
+constexpr int kManyChunk = kManyWaves * kManyBlocks * kManyBlock;  // elements of one workgroup
 
 // One tensor, as the kernels read it.
 struct ManyTensor {
@@ -21,7 +23,7 @@ struct ManyTensor {
     int64_t chunk0;  // its first chunk
     int64_t elem0;   // its first element in the padded order
     int32_t group;
-    int32_t wide;    // bit 0: every array allows the wide path; bit 1: the gradient does
+    int32_t wide;    // every array allows the wide path
 };
 
 struct ManyScalars {

@@ -6,9 +6,8 @@
 namespace zmi {
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kWaves = kThreads / 64;
-static_assert(kWaves * kManyBlock == kManyChunk, "a wave updates one block");
+constexpr int kWaves = kManyWaves;
+constexpr int kThreads = kWaves * 64;
 
 template <typename T>
 __device__ __forceinline__ __attribute__((address_space(1))) T* gptr(uint64_t addr) {
@@ -16,6 +15,57 @@ __device__ __forceinline__ __attribute__((address_space(1))) T* gptr(uint64_t ad
 }
 
 // ------------------------------------------------------------ norm
+// A workgroup sweeps tiles of kNormTile chunks, kNormVecs vectors of 16
+// bytes under way in each thread; within a tile it walks the runs of chunks
+// that one tensor holds.
+constexpr int kNormTile = 2;
+constexpr int kNormVecs = 4;
+
+// Sum of squares and nonfinite test of one 16-byte vector.
+template <int DT>
+__device__ __forceinline__ void norm_vec(const u32x4& q, double& sum, bool& bad) {
+    constexpr int per = DT == ZERO_F32 ? 4 : 8;
+#pragma unroll
+    for (int e = 0; e < per; ++e) {
+        const uint32_t x = DT == ZERO_F32 ? q[e] : (q[e >> 1] >> (16 * (e & 1))) & 0xFFFFu;
+        bad |= elem_nonfinite<DT>(x);
+        const double g = static_cast<double>(grad_to_f32<DT>(x));
+        sum = __builtin_fma(g, g, sum);  // the square is exact in fp64
+    }
+}
+
+template <int DT>
+__device__ __forceinline__ void norm_run(uint64_t base, int64_t e0, int64_t e1, double& sum,
+                                         bool& bad) {
+    constexpr int size = DT == ZERO_F32 ? 4 : 2, per = 16 / size;
+    const uint64_t first = base + static_cast<uint64_t>(e0) * size;
+    const int n = static_cast<int>(e1 - e0);
+    // elements before the first aligned vector, and behind the last
+    const int head = min(static_cast<int>((per - first % 16 / size) % per), n);
+    const int nv = (n - head) / per;
+    const int lane = static_cast<int>(threadIdx.x);
+    const int tail = head + nv * per + lane;
+    const int edge = lane < per ? (tail < n ? tail : -1) : (lane - per < head ? lane - per : -1);
+    if (edge >= 0) {
+        u32x4 q = {0, 0, 0, 0};
+        q[0] = DT == ZERO_F32 ? *gptr<const uint32_t>(first + 4u * edge)
+                              : *gptr<const uint16_t>(first + 2u * edge);
+        norm_vec<DT>(q, sum, bad);
+    }
+    const uint64_t at = first + static_cast<uint64_t>(head) * size;
+    for (int k0 = lane; k0 < nv; k0 += kThreads * kNormVecs) {
+        u32x4 q[kNormVecs];
+#pragma unroll
+        for (int i = 0; i < kNormVecs; ++i) {
+            const int k = k0 + i * kThreads;
+            q[i] = u32x4{0, 0, 0, 0};
+            if (k < nv) q[i] = __builtin_nontemporal_load(gptr<const u32x4>(at + 16u * k));
+        }
+#pragma unroll
+        for (int i = 0; i < kNormVecs; ++i) norm_vec<DT>(q[i], sum, bad);
+    }
+}
+
 template <int DT>
 __global__ void __launch_bounds__(kThreads)
 norm_kernel(const ManyView w) {
@@ -23,21 +73,18 @@ norm_kernel(const ManyView w) {
     __shared__ int lbad[kWaves];
     double sum = 0;
     bool bad = false;
-    for (int64_t c = blockIdx.x; c < w.n_chunks; c += gridDim.x) {
-        const ManyTensor& t = w.tensors[w.chunk_tensor[c]];
-        if (t.grad == 0) continue;
-        const int64_t e0 = (c - t.chunk0) * kManyChunk;
-        const int64_t e1 = min(e0 + kManyChunk, t.numel);
-        for (int64_t e = e0 + threadIdx.x; e < e1; e += kThreads) {
-            const uint32_t x = DT == ZERO_F32 ? *gptr<const uint32_t>(t.grad + 4 * e)
-                                              : *gptr<const uint16_t>(t.grad + 2 * e);
-            bad |= elem_nonfinite<DT>(x);
-            const double g = static_cast<double>(grad_to_f32<DT>(x));
-            sum += g * g;
+    for (int64_t c0 = int64_t(blockIdx.x) * kNormTile; c0 < w.n_chunks;
+         c0 += int64_t(gridDim.x) * kNormTile) {
+        const int64_t c1 = min(c0 + kNormTile, w.n_chunks);
+        for (int64_t c = c0; c < c1;) {
+            const ManyTensor& t = w.tensors[w.chunk_tensor[c]];
+            const int64_t e0 = (c - t.chunk0) * kManyChunk;
+            const int64_t e1 = min(e0 + (c1 - c) * kManyChunk, t.numel);
+            if (t.grad != 0) norm_run<DT>(t.grad, e0, e1, sum, bad);
+            c += (e1 - e0 + kManyChunk - 1) / kManyChunk;
         }
     }
-#pragma unroll
-    for (int d = 32; d > 0; d >>= 1) sum += __shfl_xor(sum, d);
+    sum = wave_sum(sum);
     const bool any = __ballot(bad) != 0ull;
     if ((threadIdx.x & 63) == 0) {
         lsum[threadIdx.x >> 6] = sum;
@@ -65,12 +112,15 @@ norm_join_kernel(const double* __restrict__ part, const int32_t* __restrict__ pa
     __shared__ int lbad[kWaves];
     double sum = 0;
     bool bad = false;
-    for (int i = threadIdx.x; i < n; i += kThreads) {
-        sum += part[i];
-        bad |= part_flag[i] != 0;
-    }
 #pragma unroll
-    for (int d = 32; d > 0; d >>= 1) sum += __shfl_xor(sum, d);
+    for (int j = 0; j < kNormParts / kThreads; ++j) {
+        const int i = j * kThreads + static_cast<int>(threadIdx.x);
+        if (i < n) {
+            sum += part[i];
+            bad |= part_flag[i] != 0;
+        }
+    }
+    sum = wave_sum(sum);
     const bool any = __ballot(bad) != 0ull;
     if ((threadIdx.x & 63) == 0) {
         lsum[threadIdx.x >> 6] = sum;
@@ -234,10 +284,8 @@ __device__ __forceinline__ void unpack_v(uint32_t w, int scale, float (&v)[4]) {
 
 // Exponent field of the largest |x| of the wave's block (NaNs aside).
 __device__ __forceinline__ int block_exponent(const float (&x)[4]) {
-    float m = fmaxf(fmaxf(fabsf(x[0]), fabsf(x[1])), fmaxf(fabsf(x[2]), fabsf(x[3])));
-#pragma unroll
-    for (int d = 32; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor(m, d));
-    return m == m ? static_cast<int>(__float_as_uint(m) >> 23) : 0;
+    const float m = fmaxf(fmaxf(fabsf(x[0]), fabsf(x[1])), fmaxf(fabsf(x[2]), fabsf(x[3])));
+    return static_cast<int>(__float_as_uint(wave_max(fmaxf(m, 0.f), 0.f)) >> 23);
 }
 
 __device__ __forceinline__ uint32_t pack_m(const float (&m)[4], int scale) {
@@ -279,53 +327,143 @@ __device__ __forceinline__ uint32_t pack_v(const float (&v)[4], int scale, uint6
     return w;
 }
 
-// A wave updates one block of 256 elements, four consecutive ones a lane.
+// What a wave holds of one block: four consecutive elements a lane.
+template <int GDT, int BITS>
+struct Block {
+    float g[4], p[4], m[4], v[4];
+    uint32_t mc, vc;  // 8-bit codes
+    int ms, vs;
+
+    __device__ __forceinline__ void load(const ManyTensor& t, int64_t blk, int64_t e, int n,
+                                         bool wide) {
+        load_grad4<GDT>(t.grad, e, n, wide, g);
+        load4(t.master, e, n, wide, p);
+        if (BITS == 8) {
+            ms = *gptr<const uint8_t>(t.m_scale + blk);
+            vs = *gptr<const uint8_t>(t.v_scale + blk);
+            mc = load_codes(t.m, e, n, wide);
+            vc = load_codes(t.v, e, n, wide);
+        } else {
+            load4(t.m, e, n, wide, m);
+            load4(t.v, e, n, wide, v);
+        }
+    }
+
+    template <int PDT>
+    __device__ __forceinline__ void step(const ManyTensor& t, const ManyScalars& sc, uint32_t key,
+                                         int64_t blk, int64_t e, int n, bool wide) {
+        if (BITS == 8) {
+            unpack_m(mc, ms, m);
+            unpack_v(vc, vs, v);
+        }
+        if (sc.adamw) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) adam_elem<true>(g[i], p[i], m[i], v[i], sc.a);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) adam_elem<false>(g[i], p[i], m[i], v[i], sc.a);
+        }
+        store4(t.master, e, n, wide, p);
+        if (PDT != 0) store_half4<PDT>(t.param, e, n, wide, p);
+        if (BITS == 8) {
+            ms = block_exponent(m);
+            vs = block_exponent(v);
+            store_codes(t.m, e, n, wide, pack_m(m, ms));
+            store_codes(t.v, e, n, wide, pack_v(v, vs, static_cast<uint64_t>(t.elem0 + e), key));
+            if ((threadIdx.x & 63) == 0) {
+                *gptr<uint8_t>(t.m_scale + blk) = static_cast<uint8_t>(ms);
+                *gptr<uint8_t>(t.v_scale + blk) = static_cast<uint8_t>(vs);
+            }
+        } else {
+            store4(t.m, e, n, wide, m);
+            store4(t.v, e, n, wide, v);
+        }
+    }
+};
+
+// Wave w of a chunk takes its blocks w, w + 4, w + 8 and w + 12, so that a
+// short tensor's blocks still spread over the waves.  Where all four are
+// whole and aligned, everything they read is under way before any of it is
+// used.
 template <int GDT, int PDT, int BITS>
 __global__ void __launch_bounds__(kThreads)
 many_adam_kernel(const ManyView w) {
     const int64_t c = block_id();
     if (c >= w.n_chunks || w.block->skip != 0) return;
-    const ManyTensor& t = w.tensors[w.chunk_tensor[c]];
+    const ManyTensor t = w.tensors[w.chunk_tensor[c]];
     if (t.grad == 0) return;
-    const int64_t blk = (c - t.chunk0) * kWaves + (threadIdx.x >> 6);
-    const int64_t e = blk * kManyBlock + (threadIdx.x & 63) * 4;
-    if (blk * kManyBlock >= t.numel) return;  // the whole wave leaves together
-    const int n = static_cast<int>(min(max(t.numel - e, int64_t(0)), int64_t(4)));
-    const bool wide = (t.wide & 1) != 0 && n == 4;
-    const ManyScalars& sc = w.block->sc[t.group];
-    float g[4], p[4], m[4], v[4];
-    load_grad4<GDT>(t.grad, e, n, wide, g);
-    load4(t.master, e, n, wide, p);
-    if (BITS == 8) {
-        const int ms = *gptr<const uint8_t>(t.m_scale + blk);
-        const int vs = *gptr<const uint8_t>(t.v_scale + blk);
-        unpack_m(load_codes(t.m, e, n, wide), ms, m);
-        unpack_v(load_codes(t.v, e, n, wide), vs, v);
-    } else {
-        load4(t.m, e, n, wide, m);
-        load4(t.v, e, n, wide, v);
-    }
-    if (sc.adamw) {
+    const ManyScalars sc = w.block->sc[t.group];
+    const uint32_t key = w.block->key;
+    const int lane = static_cast<int>(threadIdx.x & 63);
+    const int64_t chunk0 = (c - t.chunk0) * (kWaves * kManyBlocks);
+    const int64_t blk0 = chunk0 + (threadIdx.x >> 6);
+    if (t.wide && (chunk0 + kWaves * kManyBlocks) * kManyBlock <= t.numel) {
+        Block<GDT, BITS> b[kManyBlocks];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) adam_elem<true>(g[i], p[i], m[i], v[i], sc.a);
-    } else {
+        for (int i = 0; i < kManyBlocks; ++i) {
+            const int64_t blk = blk0 + i * kWaves;
+            b[i].load(t, blk, blk * kManyBlock + lane * 4, 4, true);
+        }
 #pragma unroll
-        for (int i = 0; i < 4; ++i) adam_elem<false>(g[i], p[i], m[i], v[i], sc.a);
+        for (int i = 0; i < kManyBlocks; ++i) {
+            const int64_t blk = blk0 + i * kWaves;
+            b[i].template step<PDT>(t, sc, key, blk, blk * kManyBlock + lane * 4, 4, true);
+        }
+        return;
     }
-    store4(t.master, e, n, wide, p);
-    if (PDT != 0) store_half4<PDT>(t.param, e, n, wide, p);
-    if (BITS == 8) {
-        const int ms = block_exponent(m), vs = block_exponent(v);
-        store_codes(t.m, e, n, wide, pack_m(m, ms));
-        store_codes(t.v, e, n, wide, pack_v(v, vs, static_cast<uint64_t>(t.elem0 + e),
-                                            w.block->key));
-        if ((threadIdx.x & 63) == 0) {
-            *gptr<uint8_t>(t.m_scale + blk) = static_cast<uint8_t>(ms);
-            *gptr<uint8_t>(t.v_scale + blk) = static_cast<uint8_t>(vs);
+#pragma unroll 1
+    for (int i = 0; i < kManyBlocks; ++i) {
+        const int64_t blk = blk0 + i * kWaves;
+        if (blk * kManyBlock >= t.numel) return;
+        const int64_t e = blk * kManyBlock + lane * 4;
+        const int n = static_cast<int>(min(max(t.numel - e, int64_t(0)), int64_t(4)));
+        const bool wide = t.wide && n == 4;
+        Block<GDT, BITS> b;
+        b.load(t, blk, e, n, wide);
+        b.template step<PDT>(t, sc, key, blk, e, n, wide);
+    }
+}
+
+// One block of one moment as fp32.
+template <int BITS, bool SECOND>
+__device__ __forceinline__ void moment4(const ManyTensor& t, int64_t blk, int64_t e, int n,
+                                        bool wide, float (&x)[4]) {
+    const uint64_t base = SECOND ? t.v : t.m;
+    if (BITS == 32) return load4(base, e, n, wide, x);
+    const uint32_t codes = load_codes(base, e, n, wide);
+    const int scale = *gptr<const uint8_t>((SECOND ? t.v_scale : t.m_scale) + blk);
+    if (SECOND) unpack_v(codes, scale, x);
+    else unpack_m(codes, scale, x);
+}
+
+template <int BITS, bool SECOND>
+__device__ __forceinline__ void write_values(const ManyTensor& t, int64_t chunk0, int64_t blk0,
+                                             int lane, float* out) {
+    const bool whole = t.wide && (chunk0 + kWaves * kManyBlocks) * kManyBlock <= t.numel;
+    float x[kManyBlocks][4];
+    if (whole) {
+#pragma unroll
+        for (int i = 0; i < kManyBlocks; ++i) {
+            const int64_t blk = blk0 + i * kWaves;
+            moment4<BITS, SECOND>(t, blk, blk * kManyBlock + lane * 4, 4, true, x[i]);
         }
     } else {
-        store4(t.m, e, n, wide, m);
-        store4(t.v, e, n, wide, v);
+        for (int i = 0; i < kManyBlocks; ++i) {
+            const int64_t blk = blk0 + i * kWaves, e = blk * kManyBlock + lane * 4;
+            const int n = static_cast<int>(min(max(t.numel - e, int64_t(0)), int64_t(4)));
+            if (blk * kManyBlock < t.numel) {
+                moment4<BITS, SECOND>(t, blk, e, n, t.wide && n == 4, x[i]);
+            }
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < kManyBlocks; ++i) {
+        const int64_t blk = blk0 + i * kWaves;
+        if (whole || blk * kManyBlock < t.numel) {
+            __builtin_nontemporal_store(
+                f32x4{x[i][0], x[i][1], x[i][2], x[i][3]},
+                reinterpret_cast<f32x4*>(out + t.elem0 + blk * kManyBlock + lane * 4));
+        }
     }
 }
 
@@ -334,29 +472,12 @@ __global__ void __launch_bounds__(kThreads)
 many_values_kernel(const ManyView w, float* __restrict__ mo, float* __restrict__ vo) {
     const int64_t c = block_id();
     if (c >= w.n_chunks) return;
-    const ManyTensor& t = w.tensors[w.chunk_tensor[c]];
-    const int64_t blk = (c - t.chunk0) * kWaves + (threadIdx.x >> 6);
-    const int64_t e = blk * kManyBlock + (threadIdx.x & 63) * 4;
-    if (blk * kManyBlock >= t.numel) return;
-    const int n = static_cast<int>(min(max(t.numel - e, int64_t(0)), int64_t(4)));
-    const bool wide = (t.wide & 1) != 0 && n == 4;
-    float x[4];
-    if (mo != nullptr) {
-        if (BITS == 8) {
-            unpack_m(load_codes(t.m, e, n, wide), *gptr<const uint8_t>(t.m_scale + blk), x);
-        } else {
-            load4(t.m, e, n, wide, x);
-        }
-        *reinterpret_cast<f32x4*>(mo + t.elem0 + e) = f32x4{x[0], x[1], x[2], x[3]};
-    }
-    if (vo != nullptr) {
-        if (BITS == 8) {
-            unpack_v(load_codes(t.v, e, n, wide), *gptr<const uint8_t>(t.v_scale + blk), x);
-        } else {
-            load4(t.v, e, n, wide, x);
-        }
-        *reinterpret_cast<f32x4*>(vo + t.elem0 + e) = f32x4{x[0], x[1], x[2], x[3]};
-    }
+    const ManyTensor t = w.tensors[w.chunk_tensor[c]];
+    const int64_t chunk0 = (c - t.chunk0) * (kWaves * kManyBlocks);
+    const int64_t blk0 = chunk0 + (threadIdx.x >> 6);
+    const int lane = static_cast<int>(threadIdx.x & 63);
+    if (mo != nullptr) write_values<BITS, false>(t, chunk0, blk0, lane, mo);
+    if (vo != nullptr) write_values<BITS, true>(t, chunk0, blk0, lane, vo);
 }
 
 template <int GDT, int PDT>
@@ -380,7 +501,8 @@ void adam_param(const ManyView& w, int pdt, int bits, hipStream_t s) {
 
 hipError_t launch_many_norm(const ManyView& w, int grad_dtype, double* sumsq, int32_t* flag,
                             hipStream_t s) {
-    const int parts = static_cast<int>(w.n_chunks < kNormParts ? w.n_chunks : kNormParts);
+    const int64_t tiles = (w.n_chunks + kNormTile - 1) / kNormTile;
+    const int parts = static_cast<int>(tiles < kNormParts ? tiles : kNormParts);
     if (parts > 0) {
         const dim3 grid(static_cast<unsigned>(parts));
         if (grad_dtype == ZERO_F16) {
