@@ -8,7 +8,7 @@
 namespace zmi {
 
 constexpr int kManyBlock = ZERO_MANY_BLOCK;   // elements of one 8-bit scale
-constexpr int kManyBlocks = 4;                // blocks of one wave of the update
+constexpr int kManyBlocks = 2;                // blocks of one wave of the update
 constexpr int kManyWaves = 4;                 // waves of one workgroup
 constexpr int kManyChunk = kManyWaves * kManyBlocks * kManyBlock;  // elements of one workgroup
 

@@ -190,7 +190,7 @@ many_prologue_kernel(ManyBlock* __restrict__ b, const ManyHparams hp, int n_grou
 // Four consecutive elements of a lane, wide where the tensor allows it.
 __device__ __forceinline__ void load4(uint64_t base, int64_t e, int n, bool wide, float (&x)[4]) {
     if (wide) {
-        const f32x4 q = *gptr<const f32x4>(base + 4 * e);
+        const f32x4 q = __builtin_nontemporal_load(gptr<const f32x4>(base + 4 * e));
 #pragma unroll
         for (int i = 0; i < 4; ++i) x[i] = q[i];
     } else {
@@ -202,7 +202,7 @@ __device__ __forceinline__ void load4(uint64_t base, int64_t e, int n, bool wide
 __device__ __forceinline__ void store4(uint64_t base, int64_t e, int n, bool wide,
                                        const float (&x)[4]) {
     if (wide) {
-        *gptr<f32x4>(base + 4 * e) = f32x4{x[0], x[1], x[2], x[3]};
+        __builtin_nontemporal_store(f32x4{x[0], x[1], x[2], x[3]}, gptr<f32x4>(base + 4 * e));
     } else {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -216,7 +216,7 @@ __device__ __forceinline__ void load_grad4(uint64_t base, int64_t e, int n, bool
                                            float (&x)[4]) {
     if (DT == ZERO_F32) return load4(base, e, n, wide, x);
     if (wide) {
-        const u32x2 q = *gptr<const u32x2>(base + 2 * e);
+        const u32x2 q = __builtin_nontemporal_load(gptr<const u32x2>(base + 2 * e));
 #pragma unroll
         for (int i = 0; i < 4; ++i) x[i] = grad_to_f32<DT>((q[i >> 1] >> (16 * (i & 1))) & 0xFFFFu);
     } else {
@@ -234,7 +234,7 @@ __device__ __forceinline__ void store_half4(uint64_t base, int64_t e, int n, boo
 #pragma unroll
     for (int i = 0; i < 4; ++i) h[i] = f32_to_half<DT>(x[i]);
     if (wide) {
-        *gptr<u32x2>(base + 2 * e) = u32x2{h[0] | (h[1] << 16), h[2] | (h[3] << 16)};
+        __builtin_nontemporal_store(u32x2{h[0] | (h[1] << 16), h[2] | (h[3] << 16)}, gptr<u32x2>(base + 2 * e));
     } else {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -245,7 +245,7 @@ __device__ __forceinline__ void store_half4(uint64_t base, int64_t e, int n, boo
 
 // Four codes as one word, element 0 in the low byte.
 __device__ __forceinline__ uint32_t load_codes(uint64_t base, int64_t e, int n, bool wide) {
-    if (wide) return *gptr<const uint32_t>(base + e);
+    if (wide) return __builtin_nontemporal_load(gptr<const uint32_t>(base + e));
     uint32_t w = 0;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -257,7 +257,7 @@ __device__ __forceinline__ uint32_t load_codes(uint64_t base, int64_t e, int n, 
 __device__ __forceinline__ void store_codes(uint64_t base, int64_t e, int n, bool wide,
                                             uint32_t w) {
     if (wide) {
-        *gptr<uint32_t>(base + e) = w;
+        __builtin_nontemporal_store(w, gptr<uint32_t>(base + e));
     } else {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -408,6 +408,7 @@ many_adam_kernel(const ManyView w) {
         for (int i = 0; i < kManyBlocks; ++i) {
             const int64_t blk = blk0 + i * kWaves;
             b[i].template step<PDT>(t, sc, key, blk, blk * kManyBlock + lane * 4, 4, true);
+            __builtin_amdgcn_sched_barrier(0);
         }
         return;
     }
