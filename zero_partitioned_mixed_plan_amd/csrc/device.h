@@ -62,7 +62,8 @@ __device__ __forceinline__ float dpp_max(float x, float identity) {
 }
 
 // The largest value (NaNs aside).
-__device__ __forceinline__ float wave_max(float x, float identity = -__builtin_inff()) {
+__device__ __forceinline__ float wave_max(float x) {
+    const float identity = -__builtin_inff();
     x = dpp_max<0x111, 0xF>(x, identity);
     x = dpp_max<0x112, 0xF>(x, identity);
     x = dpp_max<0x114, 0xF>(x, identity);
@@ -70,6 +71,23 @@ __device__ __forceinline__ float wave_max(float x, float identity = -__builtin_i
     x = dpp_max<0x142, 0xA>(x, identity);
     x = dpp_max<0x143, 0xC>(x, identity);
     return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(x), 63));
+}
+
+template <int CTRL, int ROWS>
+__device__ __forceinline__ uint32_t dpp_max(uint32_t x) {
+    return max(x, static_cast<uint32_t>(dpp<CTRL, ROWS>(static_cast<int>(x), 0)));
+}
+
+// The largest unsigned value; one instruction a step, as 0 is its identity
+// (a float's needs a copy and a quieting besides).
+__device__ __forceinline__ uint32_t wave_max(uint32_t x) {
+    x = dpp_max<0x111, 0xF>(x);
+    x = dpp_max<0x112, 0xF>(x);
+    x = dpp_max<0x114, 0xF>(x);
+    x = dpp_max<0x118, 0xF>(x);
+    x = dpp_max<0x142, 0xA>(x);
+    x = dpp_max<0x143, 0xC>(x);
+    return static_cast<uint32_t>(__builtin_amdgcn_readlane(static_cast<int>(x), 63));
 }
 
 template <int CTRL, int ROWS>

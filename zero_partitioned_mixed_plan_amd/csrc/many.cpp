@@ -11,6 +11,11 @@ using namespace zmi;
 
 namespace {
 
+int64_t chunks_of(const zero_many* w, int64_t numel) {
+    const int64_t chunk = many_chunk(w->bits);
+    return (numel + chunk - 1) / chunk;
+}
+
 size_t up256(size_t n) { return (n + 255) / 256 * 256; }
 
 // Sections of the device allocation.
@@ -49,7 +54,7 @@ int ensure(zero_many* w, hipStream_t s) {
     std::vector<uint32_t> chunks;
     chunks.reserve(static_cast<size_t>(w->n_chunks));
     for (size_t i = 0; i < w->numels.size(); ++i) {
-        const int64_t n = (w->numels[i] + kManyChunk - 1) / kManyChunk;
+        const int64_t n = chunks_of(w, w->numels[i]);
         chunks.insert(chunks.end(), static_cast<size_t>(n), static_cast<uint32_t>(i));
     }
     void *d = nullptr, *h = nullptr;
@@ -76,6 +81,7 @@ int ensure(zero_many* w, hipStream_t s) {
     w->view.tensors = reinterpret_cast<const ManyTensor*>(w->d_mem + at.tensors);
     w->view.chunk_tensor = reinterpret_cast<const uint32_t*>(w->d_mem + at.chunks);
     w->view.n_chunks = w->n_chunks;
+    w->view.chunk = many_chunk(w->bits);
     w->device = dev;
     w->ready = true;
     return ZERO_OK;
@@ -186,7 +192,7 @@ int zero_many_create(const int64_t* numels, const int32_t* groups, int32_t n_ten
             w->offsets.push_back(w->padded);
             w->total += n;
             w->padded += (n + kManyBlock - 1) / kManyBlock * kManyBlock;
-            w->n_chunks += (n + kManyChunk - 1) / kManyChunk;
+            w->n_chunks += chunks_of(w.get(), n);
         }
         *out = w.release();
     } catch (const std::bad_alloc&) {
@@ -248,7 +254,7 @@ int zero_many_bind(zero_many_t* w, const zero_many_buffers_t* b, void* stream) {
         for (size_t i = 0; i < table.size(); ++i) {
             const int rc = fill_tensor(w, b, i, chunk, &table[i]);
             if (rc != ZERO_OK) return rc;
-            chunk += (w->numels[i] + kManyChunk - 1) / kManyChunk;
+            chunk += chunks_of(w, w->numels[i]);
         }
         if (capturing(s)) return fail(ZERO_ESTATE, "zero_many_bind cannot be captured");
         const int rc = ensure(w, s);

@@ -8,9 +8,14 @@
 namespace zmi {
 
 constexpr int kManyBlock = ZERO_MANY_BLOCK;   // elements of one 8-bit scale
-constexpr int kManyBlocks = 2;                // blocks of one wave of the update
-constexpr int kManyWaves = 4;                 // waves of one workgroup
-constexpr int kManyChunk = kManyWaves * kManyBlocks * kManyBlock;  // elements of one workgroup
+// Elements of one workgroup of the update (a chunk; chunks start at a
+// tensor's start).  8 bits: kManyWaves waves of kManyBlocks blocks each.
+constexpr int kManyBlocks = 2;
+constexpr int kManyWaves = 4;
+constexpr int kManyPer32 = 2;  // 32 bits: elements of one thread
+constexpr int many_chunk(int bits) {
+    return bits == 8 ? kManyWaves * kManyBlocks * kManyBlock : kManyWaves * 64 * kManyPer32;
+}
 
 // One tensor, as the kernels read it.
 struct ManyTensor {
@@ -51,6 +56,7 @@ struct ManyView {
     const ManyTensor* tensors;
     const uint32_t* chunk_tensor;  // the tensor of each chunk
     int64_t n_chunks;
+    int64_t chunk;  // many_chunk of the handle
     ManyBlock* block;
     double* part;        // [kNormParts] sums of squares
     int32_t* part_flag;  // [kNormParts]
