@@ -632,7 +632,8 @@ policy_kernel(const typename Elem<DT>::T* logits, int64_t rows, int vocab, int64
         if (weight != nullptr) in.weight = weight[r];
     }
     if (VPT > 0) {
-        constexpr int kGroup = VPT < 4 ? VPT : 4;
+        constexpr int kGroup = 4;
+        static_assert(VPT % kGroup == 0, "whole groups");
         Running run;
 #pragma unroll
         for (int i0 = 0; i0 < VPT; i0 += kGroup) {
@@ -796,26 +797,37 @@ void with_dtype(int32_t dtype, F f) {
 // arithmetic on its one CU is what it waits for.)
 constexpr int64_t kFewRows = 256;
 
-// Calls f with the threads that take a row of nv vectors.
+// Calls f with the threads that take a row of nv vectors.  16384 rows of
+// 8192 half logits took 35 us with 128 threads and 38 with 64 or 256; of
+// 16384, 65 with 256 and 69 with 512; 8192 rows of 32000, 64 with 512 and 67
+// with 256; 4096 rows of 50257, 55 with 512 and 62 with 256 or 1024.
 template <typename F>
 void with_threads(int64_t nv, int64_t rows, F f) {
     if (rows <= kFewRows && nv > 256 * 4) f(Const<1024>());
-    else if (nv <= 64 * 8 && rows >= 2048) f(Const<64>());
-    else if (nv <= 256 * 16) f(Const<256>());
+    else if (rows <= kFewRows) f(Const<256>());
+    else if (nv <= 64 * 8) f(Const<64>());
+    else if (nv <= 128 * 8) f(Const<128>());
+    else if (nv <= 256 * 8) f(Const<256>());
     else if (nv <= 512 * 16) f(Const<512>());
     else f(Const<1024>());
 }
 
 // The threads and vectors per thread of a kernel that keeps the row in
-// registers (0: the row does not fit).
+// registers (0: the row does not fit).  Many threads with four vectors each
+// pass a row on sooner than few with more: 16384 rows of 2000, 4096 and 16384
+// half logits took 31, 50 and 170 us with 64, 128 and 512 threads, and 35, 52
+// and 181 with 64 x 8, 64 x 8 and 256 x 8; 8192 rows of 32000 took 163 us
+// with 1024 x 4, 169 with 512 x 8 and 182 with 256 x 16.  Longer rows need
+// two workgroups on a CU more than they need threads: 4096 rows of 50257 took
+// 149 us with 512 x 16 and 171 with 1024 x 8.
 template <typename F>
 void with_row_shape(int64_t nv, int64_t rows, F f) {
-    if (rows <= kFewRows && nv > 256 * 4 && nv <= 1024 * 4) f(Const<1024>(), Const<4>());
-    else if (rows <= kFewRows && nv > 1024 * 4 && nv <= 1024 * 8) f(Const<1024>(), Const<8>());
-    else if (nv <= 64 * 8 && rows >= 2048) f(Const<64>(), Const<8>());
+    if (nv <= 64 * 4) f(Const<64>(), Const<4>());
+    else if (nv <= 128 * 4) f(Const<128>(), Const<4>());
     else if (nv <= 256 * 4) f(Const<256>(), Const<4>());
-    else if (nv <= 256 * 8) f(Const<256>(), Const<8>());
-    else if (nv <= 256 * 16) f(Const<256>(), Const<16>());
+    else if (nv <= 512 * 4) f(Const<512>(), Const<4>());
+    else if (nv <= 1024 * 4) f(Const<1024>(), Const<4>());
+    else if (nv <= 1024 * 8 && rows <= kFewRows) f(Const<1024>(), Const<8>());
     else if (nv <= 512 * 16) f(Const<512>(), Const<16>());
     else if (nv <= 1024 * 16) f(Const<1024>(), Const<16>());
     else f(Const<1024>(), Const<0>());
