@@ -438,6 +438,66 @@ __device__ __forceinline__ double softplus(double y) {
     return fmax(y, 0.0) + log1p(exp(-fabs(y)));
 }
 
+struct PairOut {
+    double loss;
+    float slope[2];  // dlogp of the chosen and the rejected sequence's tokens
+};
+
+// One pair from the sums of its sequences' log ratios and their tokens.
+__device__ __forceinline__ PairOut pair_loss_of(double sum0, double n0, double sum1, double n1,
+                                                const zero_preference_t& cfg, double scale,
+                                                int64_t i, float* pair_loss, float* rewards) {
+    if (!cfg.average || n0 < 1) n0 = 1;
+    if (!cfg.average || n1 < 1) n1 = 1;
+    const double d0 = sum0 / n0, d1 = sum1 / n1;
+    const double beta = cfg.beta, e = cfg.label_smoothing, delta = d0 - d1;
+    double loss, dd;
+    if (cfg.kind == ZERO_PREF_SQUARED) {
+        const double u = delta - 1.0 / (2.0 * beta);
+        loss = u * u;
+        dd = 2.0 * u;
+    } else {
+        const double h = beta * delta;
+        loss = (1.0 - e) * softplus(-h) + e * softplus(h);
+        dd = beta * (e / (1.0 + exp(-h)) - (1.0 - e) / (1.0 + exp(h)));
+    }
+    pair_loss[i] = static_cast<float>(loss);
+    rewards[2 * i] = static_cast<float>(beta * d0);
+    rewards[2 * i + 1] = static_cast<float>(beta * d1);
+    PairOut o;
+    o.loss = loss;
+    o.slope[0] = static_cast<float>(scale * cfg.norm * dd / n0);
+    o.slope[1] = static_cast<float>(-(scale * cfg.norm * dd) / n1);
+    return o;
+}
+
+// Sum of a sequence's log ratios over its unmasked tokens, and their number,
+// by T threads of which this is `lane`.
+template <int T>
+__device__ __forceinline__ void sequence_sums(const float* logp, const float* ref,
+                                              const int64_t* labels, int64_t a, int64_t b,
+                                              int lane, double* sum, double* n) {
+    double s = 0, c = 0;
+#pragma unroll 4
+    for (int64_t t = a + lane; t < b; t += T) {
+        const bool live = labels == nullptr || labels[t] >= 0;
+        const double x = static_cast<double>(logp[t]) -
+                         (ref != nullptr ? static_cast<double>(ref[t]) : 0.0);
+        s += live ? x : 0.0;  // a masked token's scores may be anything
+        c += live ? 1.0 : 0.0;
+    }
+    *sum = s;
+    *n = c;
+}
+
+// A sequence's tokens; offsets outside [0, rows] would reach past the buffers.
+__device__ __forceinline__ void sequence_range(const int64_t* seq, int64_t s, int64_t rows,
+                                               int64_t* a, int64_t* b) {
+    *a = min(max(seq[s], int64_t(0)), rows);
+    *b = min(max(seq[s + 1], int64_t(0)), rows);
+}
+
+// A workgroup per pair.
 __global__ void __launch_bounds__(kRowThreads)
 preference_kernel(const float* __restrict__ logp, const float* __restrict__ ref,
                   const int64_t* __restrict__ labels, int64_t rows,
@@ -449,47 +509,27 @@ preference_kernel(const float* __restrict__ logp, const float* __restrict__ ref,
     __shared__ float slope[2];
     const int64_t i = block_id();
     if (i >= pairs) return;
+    const int lane = static_cast<int>(threadIdx.x);
     int64_t a[2], b[2];
     double d[2], n[2];
 #pragma unroll
     for (int s = 0; s < 2; ++s) {
-        // offsets outside [0, rows] would reach past the buffers
-        a[s] = min(max(seq[2 * i + s], int64_t(0)), rows);
-        b[s] = min(max(seq[2 * i + s + 1], int64_t(0)), rows);
-        double sum = 0, cnt = 0;
-        for (int64_t t = a[s] + threadIdx.x; t < b[s]; t += kRowThreads) {
-            if (labels != nullptr && labels[t] < 0) continue;
-            sum += static_cast<double>(logp[t]) - (ref != nullptr ? static_cast<double>(ref[t]) : 0.0);
-            cnt += 1;
-        }
-        d[s] = block_sum<kRowThreads / 64>(sum, lds[2 * s]);
-        n[s] = block_sum<kRowThreads / 64>(cnt, lds[2 * s + 1]);
-        if (!cfg.average || n[s] < 1) n[s] = 1;
-        d[s] /= n[s];
+        sequence_range(seq, 2 * i + s, rows, &a[s], &b[s]);
+        sequence_sums<kRowThreads>(logp, ref, labels, a[s], b[s], lane, &d[s], &n[s]);
+        d[s] = block_sum<kRowThreads / 64>(d[s], lds[2 * s]);
+        n[s] = block_sum<kRowThreads / 64>(n[s], lds[2 * s + 1]);
     }
     if (threadIdx.x == 0) {
-        const double beta = cfg.beta, e = cfg.label_smoothing, delta = d[0] - d[1];
-        double loss, dd;
-        if (cfg.kind == ZERO_PREF_SQUARED) {
-            const double u = delta - 1.0 / (2.0 * beta);
-            loss = u * u;
-            dd = 2.0 * u;
-        } else {
-            const double h = beta * delta;
-            loss = (1.0 - e) * softplus(-h) + e * softplus(h);
-            dd = beta * (e / (1.0 + exp(-h)) - (1.0 - e) / (1.0 + exp(h)));
-        }
-        pair_loss[i] = static_cast<float>(loss);
-        rewards[2 * i] = static_cast<float>(beta * d[0]);
-        rewards[2 * i + 1] = static_cast<float>(beta * d[1]);
-        const double k = (scale_dev != nullptr ? *scale_dev : scale_host) * cfg.norm * dd;
-        slope[0] = static_cast<float>(k / n[0]);
-        slope[1] = static_cast<float>(-k / n[1]);
+        const PairOut o = pair_loss_of(d[0], n[0], d[1], n[1], cfg,
+                                       scale_dev != nullptr ? *scale_dev : scale_host, i,
+                                       pair_loss, rewards);
+        slope[0] = o.slope[0];
+        slope[1] = o.slope[1];
     }
     __syncthreads();
 #pragma unroll
     for (int s = 0; s < 2; ++s) {
-        for (int64_t t = a[s] + threadIdx.x; t < b[s]; t += kRowThreads) {
+        for (int64_t t = a[s] + lane; t < b[s]; t += kRowThreads) {
             dlogp[t] = labels != nullptr && labels[t] < 0 ? 0.f : slope[s];
         }
     }
@@ -519,6 +559,59 @@ sum_kernel(const float* __restrict__ x, int64_t n, double norm, float* __restric
     s = block_sum<kSumThreads / 64>(s, lds);
     if (threadIdx.x == 0) *loss = static_cast<float>(norm * s);
 }
+
+// One workgroup for a whole small batch, a wave per pair: the batch's loss
+// comes with it, without a second launch.
+__global__ void __launch_bounds__(kSumThreads)
+preference_small_kernel(const float* __restrict__ logp, const float* __restrict__ ref,
+                        const int64_t* __restrict__ labels, int64_t rows,
+                        const int64_t* __restrict__ seq, int64_t pairs,
+                        const zero_preference_t cfg, double scale_host,
+                        const double* __restrict__ scale_dev, float* __restrict__ loss,
+                        float* __restrict__ pair_loss, float* __restrict__ rewards,
+                        float* __restrict__ dlogp) {
+    __shared__ double lds[kSumThreads / 64];
+    const int lane = static_cast<int>(threadIdx.x & 63);
+    const double scale = scale_dev != nullptr ? *scale_dev : scale_host;
+    double total = 0;
+    for (int64_t i = threadIdx.x >> 6; i < pairs; i += kSumThreads / 64) {
+        int64_t a[2], b[2];
+        double d[2], n[2];
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+            sequence_range(seq, 2 * i + s, rows, &a[s], &b[s]);
+            sequence_sums<64>(logp, ref, labels, a[s], b[s], lane, &d[s], &n[s]);
+        }
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+            d[s] = wave_sum(d[s]);
+            n[s] = wave_sum(n[s]);
+        }
+        // the same value in every lane; each writes it to the same place
+        const PairOut o = pair_loss_of(d[0], n[0], d[1], n[1], cfg, scale, i, pair_loss, rewards);
+        // as the other form adds them: the pairs' losses as they are stored
+        total += static_cast<double>(static_cast<float>(o.loss));
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+            for (int64_t t = a[s] + lane; t < b[s]; t += 64) {
+                dlogp[t] = labels != nullptr && labels[t] < 0 ? 0.f : o.slope[s];
+            }
+        }
+    }
+    if (lane == 0) lds[threadIdx.x >> 6] = total;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        total = 0;
+        for (int w = 0; w < kSumThreads / 64; ++w) total += lds[w];
+        *loss = static_cast<float>(cfg.norm * total);
+    }
+}
+
+// Up to here one workgroup takes the whole batch: a wave has two pairs at
+// most, and a sequence of a few hundred tokens a few rounds of loads, which
+// together cost less than the launch that they save (2 pairs of 24 tokens
+// went from 27 to 24 us with their scores and gradients).
+constexpr int64_t kSmallTokens = 1024, kSmallPairs = 2 * (kSumThreads / 64);
 
 // ------------------------------------------------------------ policy
 struct PolicyTerms {
@@ -927,6 +1020,12 @@ int zero_preference_loss(const float* logp, const float* ref_logp, const int64_t
         return fail(ZERO_EALIGN, "labels and seq_offsets must be 8-byte aligned");
     }
     hipStream_t s = static_cast<hipStream_t>(stream);
+    if (rows <= kSmallTokens && pairs <= kSmallPairs) {
+        hipLaunchKernelGGL(preference_small_kernel, dim3(1), dim3(kSumThreads), 0, s, logp,
+                           ref_logp, labels, rows, seq_offsets, pairs, *cfg, loss_scale,
+                           loss_scale_dev, loss, pair_loss, rewards, dlogp);
+        return launched("preference loss launch");
+    }
     if (pairs > 0) {
         hipLaunchKernelGGL(preference_kernel, grid_2d(pairs), dim3(kRowThreads), 0, s, logp,
                            ref_logp, labels, rows, seq_offsets, pairs, *cfg, loss_scale,

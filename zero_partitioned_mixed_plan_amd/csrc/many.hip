@@ -23,6 +23,7 @@ __device__ __forceinline__ __attribute__((address_space(1))) T* gptr(uint64_t ad
 // chunks that one tensor holds.
 constexpr int64_t kNormTile = 8192;
 constexpr int kNormVecs = 4;
+constexpr int64_t kNormFew = 2;  // tiles that one workgroup takes alone
 
 // Sum of squares and nonfinite test of one 16-byte vector.
 template <int DT>
@@ -71,7 +72,7 @@ __device__ __forceinline__ void norm_run(uint64_t base, int64_t e0, int64_t e1, 
 
 template <int DT>
 __global__ void __launch_bounds__(kThreads)
-norm_kernel(const ManyView w) {
+norm_kernel(const ManyView w, double* __restrict__ sumsq, int32_t* __restrict__ flag) {
     __shared__ double lsum[kWaves];
     __shared__ int lbad[kWaves];
     double sum = 0;
@@ -102,8 +103,13 @@ norm_kernel(const ManyView w) {
             sum += lsum[i];
             f |= lbad[i];
         }
-        w.part[blockIdx.x] = sum;
-        w.part_flag[blockIdx.x] = f;
+        if (sumsq != nullptr) {  // this workgroup is the only one
+            *sumsq = sum;
+            *flag = f;
+        } else {
+            w.part[blockIdx.x] = sum;
+            w.part_flag[blockIdx.x] = f;
+        }
     }
 }
 
@@ -629,19 +635,22 @@ void adam_param(const ManyView& w, int pdt, int bits, hipStream_t s) {
 hipError_t launch_many_norm(const ManyView& w, int grad_dtype, double* sumsq, int32_t* flag,
                             hipStream_t s) {
     const int64_t tile = kNormTile / w.chunk, tiles = (w.n_chunks + tile - 1) / tile;
-    const int parts = static_cast<int>(tiles < kNormParts ? tiles : kNormParts);
-    if (parts > 0) {
-        const dim3 grid(static_cast<unsigned>(parts));
-        if (grad_dtype == ZERO_F16) {
-            hipLaunchKernelGGL(norm_kernel<ZERO_F16>, grid, dim3(kThreads), 0, s, w);
-        } else if (grad_dtype == ZERO_BF16) {
-            hipLaunchKernelGGL(norm_kernel<ZERO_BF16>, grid, dim3(kThreads), 0, s, w);
-        } else {
-            hipLaunchKernelGGL(norm_kernel<ZERO_F32>, grid, dim3(kThreads), 0, s, w);
-        }
+    // a few tiles are one workgroup's, which then needs no second launch
+    const bool one = tiles <= kNormFew;
+    const int parts = static_cast<int>(one ? 1 : tiles < kNormParts ? tiles : kNormParts);
+    const dim3 grid(static_cast<unsigned>(parts));
+    double* out = one ? sumsq : nullptr;
+    if (grad_dtype == ZERO_F16) {
+        hipLaunchKernelGGL(norm_kernel<ZERO_F16>, grid, dim3(kThreads), 0, s, w, out, flag);
+    } else if (grad_dtype == ZERO_BF16) {
+        hipLaunchKernelGGL(norm_kernel<ZERO_BF16>, grid, dim3(kThreads), 0, s, w, out, flag);
+    } else {
+        hipLaunchKernelGGL(norm_kernel<ZERO_F32>, grid, dim3(kThreads), 0, s, w, out, flag);
     }
-    hipLaunchKernelGGL(norm_join_kernel, dim3(1), dim3(kThreads), 0, s, w.part, w.part_flag, parts,
-                       sumsq, flag);
+    if (!one) {
+        hipLaunchKernelGGL(norm_join_kernel, dim3(1), dim3(kThreads), 0, s, w.part, w.part_flag,
+                           parts, sumsq, flag);
+    }
     return hipGetLastError();
 }
 
