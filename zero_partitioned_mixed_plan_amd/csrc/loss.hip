@@ -250,6 +250,14 @@ __device__ __forceinline__ double label_logp(float raw_label, int64_t label, int
 template <int T>
 constexpr int rows_per_group() { return T == 64 ? 4 : 1; }
 
+// The row of this thread, known to be uniform over its wave.
+template <int T>
+__device__ __forceinline__ int64_t row_id() {
+    if (T > 64) return block_id();
+    return block_id() * rows_per_group<T>() +
+           __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x >> 6));
+}
+
 template <int DT, int T>
 __global__ void __launch_bounds__(T * rows_per_group<T>())
 logp_kernel(const typename Elem<DT>::T* __restrict__ logits, int64_t rows, int vocab,
@@ -257,7 +265,7 @@ logp_kernel(const typename Elem<DT>::T* __restrict__ logits, int64_t rows, int v
             float* __restrict__ logp, float* __restrict__ lse) {
     __shared__ RowStats part[T / 64];
     const int lane = static_cast<int>(threadIdx.x) % T;
-    const int64_t r = block_id() * rows_per_group<T>() + threadIdx.x / T;
+    const int64_t r = row_id<T>();
     if (r >= rows) return;
     const int64_t label = labels[r];
     if (label < 0) {
@@ -691,7 +699,7 @@ policy_kernel(const typename Elem<DT>::T* logits, int64_t rows, int vocab, int64
     __shared__ RowStats part[T / 64];
     __shared__ RowGrad share;
     const int lane = static_cast<int>(threadIdx.x) % T;
-    const int64_t r = block_id() * rows_per_group<T>() + threadIdx.x / T;
+    const int64_t r = row_id<T>();
     if (r >= rows) return;
     const int64_t label = labels[r];
     const auto* row = logits + r * stride;
