@@ -525,7 +525,9 @@ int zero_adam_scalars(const zero_adam_hparams_t* hp, int64_t t_first, int64_t co
  *   lse  = log sum_j exp(x_j)        logp = x_label - lse
  * A row whose logits are all -inf has lse = logp = -inf and a zero gradient;
  * NaN and +inf logits give NaN.  Maxima, sums and logarithms are held in
- * fp32 or more (sums across a row's threads in fp64).
+ * fp32 or more (sums across a row's threads in fp64).  What passes from one
+ * call to the next (logp, lse, dlogp) is fp32: a score is off by half a step
+ * of its own size, 2^-24 |logp|, and a reward by its tokens' sum of those.
  *
  * loss_scale multiplies the gradients (not the losses); when loss_scale_dev
  * is not NULL, the double it points to in device memory is used instead
@@ -533,8 +535,9 @@ int zero_adam_scalars(const zero_adam_hparams_t* hp, int64_t t_first, int64_t co
  * ------------------------------------------------------------------------ */
 
 /* logp[r] and lse[r] of every row; both are 0 for masked rows.  lse may be
- * NULL.  Errors: ZERO_ENULL, ZERO_EINVAL (dtype, rows < 0, vocab < 1,
- * row_stride, inv_temperature not finite or <= 0), ZERO_EALIGN, ZERO_EHIP. */
+ * NULL.  Errors: ZERO_ENULL, ZERO_EINVAL (dtype, rows outside [0, 2^31],
+ * vocab outside [1, 2^30], row_stride, inv_temperature not finite or <= 0),
+ * ZERO_EALIGN, ZERO_EHIP. */
 int zero_token_logp(const void* logits, int32_t dtype, int64_t rows, int64_t vocab,
                     int64_t row_stride, const int64_t* labels, float inv_temperature,
                     float* logp, float* lse, void* stream);
@@ -685,7 +688,8 @@ typedef struct {
 } zero_many_buffers_t;
 
 /* Hands the tensors to the handle (again after any of them moved); waits
- * for `stream`, and cannot be captured.  Errors: ZERO_ENULL, ZERO_EINVAL,
+ * for `stream`, and cannot be captured.  Nothing of the handle may be in
+ * flight on another stream, and a captured graph sees the new tensors.  Errors: ZERO_ENULL, ZERO_EINVAL,
  * ZERO_EALIGN, ZERO_ESTATE (capturing, or another device), ZERO_EHIP,
  * ZERO_ENOMEM. */
 int zero_many_bind(zero_many_t* many, const zero_many_buffers_t* buffers, void* stream);

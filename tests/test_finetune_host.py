@@ -27,7 +27,7 @@ def _grad(logits=P, dtype=ZERO_BF16, rows=4, vocab=10, stride=10, labels=P, inv_
                                     dlogits, dstride, None)
 
 
-MATRIX = [(dict(dtype=0), ZERO_EINVAL), (dict(dtype=4), ZERO_EINVAL), (dict(rows=-1), ZERO_EINVAL),
+MATRIX = [(dict(rows=(1 << 31) + 1), ZERO_EINVAL), (dict(dtype=0), ZERO_EINVAL), (dict(dtype=4), ZERO_EINVAL), (dict(rows=-1), ZERO_EINVAL),
           (dict(vocab=0), ZERO_EINVAL), (dict(vocab=(1 << 30) + 1, stride=1 << 40), ZERO_EINVAL),
           (dict(stride=9), ZERO_EINVAL), (dict(rows=1 << 40, stride=1 << 40), ZERO_EINVAL),
           (dict(inv_t=0.0), ZERO_EINVAL), (dict(inv_t=-1.0), ZERO_EINVAL),

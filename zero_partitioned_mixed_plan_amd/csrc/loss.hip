@@ -823,7 +823,9 @@ int check_matrix(const void* logits, int32_t dtype, int64_t rows, int64_t vocab,
     if (!valid_grad_dtype(dtype)) {
         return fail(ZERO_EINVAL, "dtype must be ZERO_F16, ZERO_BF16 or ZERO_F32");
     }
-    if (rows < 0) return fail(ZERO_EINVAL, "rows must be >= 0");
+    if (rows < 0 || rows > (int64_t(1) << 31)) {
+        return fail(ZERO_EINVAL, "rows must be in [0, 2^31]");
+    }
     if (vocab < 1 || vocab > (int64_t(1) << 30)) {
         return fail(ZERO_EINVAL, "vocab must be in [1, 2^30]");
     }
