@@ -370,6 +370,21 @@ def test_policy_rows_with_masks_and_nan(vocab, dt):
     assert torch.equal(dl[keep], before[keep])
 
 
+def test_policy_infinite_kl_without_a_coefficient():
+    """A reference score far above the policy's: the KL is infinite, and stays out of the loss
+    and the gradient while its coefficient is 0."""
+    m = Matrix(4, 300, "f32", seed=3)
+    m.labels[:] = 5
+    m.host[0, 5] = -900.0
+    _, logits = m.device()
+    f = lambda v: torch.full((4,), v, device=DEV)
+    dl, logp, terms, loss = torch.empty_like(logits), _new(4), _new(4, 4), _new(4)
+    z.zero_policy_loss(logits, m.labels.to(DEV), f(-3.0), f(1.0), dl, logp, terms, loss,
+                       ref_logp=f(0.0), kl_coef=0.0)
+    assert math.isinf(terms[0, 1].item()) and math.isinf(loss[2].item())
+    assert torch.isfinite(loss[:2]).all() and torch.isfinite(dl).all()
+
+
 # ------------------------------------------------------- streams and graphs
 def _whole_pass(bufs, stream=None):
     logits, lab, ref, cu, logp, lse, dlogp, loss, pair, rew, dl = bufs

@@ -1,6 +1,36 @@
 // Fine-tuning losses: log-probabilities of the labels, their gradient to the
 // logits, the preference loss of pairs and the clipped policy loss, with
 // their entry points.
+//
+// With x = logits / temperature, lse = log sum exp x and logp = x_label -
+// lse, the gradient of a score is dlogp ([j = label] - exp(x_j - lse)): two
+// passes over a row, each about ten operations and one exponential per
+// logit.  At 2 bytes a logit that is memory's work, though not by much: at
+// the full rate a stream that is read leaves the vector units 10 operations
+// per logit (the scores take 8), one read and written 20 (the policy loss
+// takes 12).
+// What each form has to move, and how near it comes to the 6.5-7 TB/s that
+// a copy and a read reach (a fifth of the rows masked: not read):
+//   log-probabilities  one read; 4096 x 128256 bf16 in 126 us, 6.6 TB/s
+//   preference loss    two reads and a write, as a pair's slope needs its
+//                      every score first; 10344 x 32000 bf16 in 277 us, 6.2
+//                      TB/s (scores 80 us, pairs 10, gradient 190)
+//   policy loss        one read and a write, as a token's slope needs its own
+//                      row alone: the row waits in registers; 4096 x 128256
+//                      bf16 in 343 us, 5.5 TB/s, 8192 x 32000 in 163, 5.8
+// The policy loss is what is furthest off: a row's phases (load, reduce, the
+// token's arithmetic, store) follow one another, and a CU's registers hold
+// one row of 128256, or two of 50257, to overlap them with.  Reading such a
+// row twice instead takes 381 us, the second time mostly from a cache (502
+// where the first read streams past it); longer rows have no other way.  A
+// part of a row in LDS for a second one, or the next row's loads issued
+// between this one's stores, cost more in spilled registers than they gave
+// (413 and 463 us).
+//
+// Scores, statistics and slopes are fp32 or fp64; a gradient is rounded once,
+// to the logits' type.  The hardware's exp2 (1 ulp, results below 2^-126
+// flushed to 0) serves the exponentials per logit: a probability so small
+// adds nothing to its row and is 0 in any gradient.
 #include <cmath>
 #include <type_traits>
 
@@ -16,8 +46,8 @@ __device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_ex
 
 typedef float f32x2 __attribute__((ext_vector_type(2)));
 
-// A vector of 16 bytes at any element's address: rows start wherever their
-// stride puts them.
+// Elements as words, and a vector of 16 bytes at any element's address (V,
+// for stores: an output's rows need not be aligned as the logits' are).
 template <int DT>
 struct Elem {
     typedef uint16_t T;
@@ -95,14 +125,14 @@ __device__ __forceinline__ RowShape row_shape(const typename Elem<DT>::T* row, i
     return o;
 }
 
-template <int DT>
+template <int DT, bool STREAM = true>
 __device__ __forceinline__ u32x4 load_vec(const typename Elem<DT>::T* row, const RowShape& w,
                                           int k) {
-    return __builtin_nontemporal_load(
-        reinterpret_cast<const u32x4*>(row + w.head + k * Elem<DT>::kPer));
+    const auto* at = reinterpret_cast<const u32x4*>(row + w.head + k * Elem<DT>::kPer);
+    if constexpr (STREAM) return __builtin_nontemporal_load(at);
+    else return *at;
 }
 
-// The output's rows need not be aligned as the logits' are.
 template <int DT>
 __device__ __forceinline__ void store_vec(typename Elem<DT>::T* row, const RowShape& w, int k,
                                           const u32x4& q) {
@@ -211,8 +241,9 @@ __device__ __forceinline__ RowLse row_lse(const RowStats& st, float inv_t) {
     return o;
 }
 
-// This wave's statistics of one row, read once.
-template <int DT, int T>
+// This wave's statistics of one row.  AGAIN: the row will be read once more
+// soon, so the default cache policy keeps it near; otherwise it streams past.
+template <int DT, int T, bool AGAIN>
 __device__ __forceinline__ RowStats row_stats(const typename Elem<DT>::T* row, int vocab, float c,
                                               int lane) {
     constexpr int kGroup = 4;
@@ -224,7 +255,7 @@ __device__ __forceinline__ RowStats row_stats(const typename Elem<DT>::T* row, i
 #pragma unroll
         for (int i = 0; i < kGroup; ++i) {
             const int k = k0 + i * T;
-            q[i] = k < w.nf ? load_vec<DT>(row, w, k) : neg_inf_vec<DT>();
+            q[i] = k < w.nf ? load_vec<DT, !AGAIN>(row, w, k) : neg_inf_vec<DT>();
         }
         float g = run.m;
 #pragma unroll
@@ -258,6 +289,7 @@ __device__ __forceinline__ int64_t row_id() {
            __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x >> 6));
 }
 
+// A workgroup (T = 64: a wave) per row, read once.
 template <int DT, int T>
 __global__ void __launch_bounds__(T * rows_per_group<T>())
 logp_kernel(const typename Elem<DT>::T* __restrict__ logits, int64_t rows, int vocab,
@@ -279,7 +311,7 @@ logp_kernel(const typename Elem<DT>::T* __restrict__ logits, int64_t rows, int v
     const float c = inv_t * kLog2e;
     float raw_label = 0.f;
     if (lane == 0 && label < vocab) raw_label = grad_to_f32<DT>(row[label]);
-    RowStats st = row_stats<DT, T>(row, vocab, c, lane);
+    RowStats st = row_stats<DT, T, false>(row, vocab, c, lane);
     if (T > 64) {
         if ((lane & 63) == 0) part[lane >> 6] = st;
         __syncthreads();
@@ -373,7 +405,7 @@ __device__ __forceinline__ RowGrad grad_from_lse(float lse, float inv_t, float g
 // The gradient of given scores needs nothing across a row, so a workgroup
 // takes a tile of kTileThreads x kTileVecs vectors (4 KiB in, 4 KiB out), a
 // row's tiles in address order, as a copy would.  Against a workgroup per
-// row the preference loss of 9.7k x 32000 bf16 went from 314 to 283 us;
+// row the preference loss of 10344 x 32000 bf16 went from 314 to 283 us;
 // 256 x 2, 256 x 4, 128 x 4, 64 x 2, 64 x 4 and 128 x 1 gave 292, 305, 307,
 // 290, 297 and 295.
 constexpr int kTileThreads = 128;
@@ -640,7 +672,9 @@ __device__ __forceinline__ double policy_token(double ratio1, double q, double e
     out->kl = has_ref ? static_cast<float>(em - q) : 0.f;
     out->clipped = clipped ? 1.f : 0.f;
     out->weight = weight;
-    return (clipped ? 0.0 : -kept) - (has_ref ? static_cast<double>(cfg.kl_coef) * em : 0.0);
+    // without a coefficient an infinite KL stays out of the gradient
+    const double k = cfg.kl_coef;
+    return (clipped ? 0.0 : -kept) - (has_ref && k != 0 ? k * em : 0.0);
 }
 
 // What a row's token brings beside its logits.
@@ -748,7 +782,7 @@ policy_kernel(const typename Elem<DT>::T* logits, int64_t rows, int vocab, int64
         run.add_edge(edge, c);
         st = wave_stats(run, c);
     } else {
-        st = row_stats<DT, T>(row, vocab, c, lane);
+        st = row_stats<DT, T, true>(row, vocab, c, lane);
     }
     const double scale = scale_dev != nullptr ? *scale_dev : scale_host;
     RowGrad o;
@@ -806,7 +840,7 @@ policy_sum_kernel(const PolicyTerms* __restrict__ terms, int64_t rows, double no
 #pragma unroll
     for (int k = 0; k < 3; ++k) s[k] = norm * block_sum<kSumThreads / 64>(s[k], lds[k]);
     if (threadIdx.x == 0) {
-        loss[0] = static_cast<float>(s[0] + kl_coef * s[1]);
+        loss[0] = static_cast<float>(kl_coef != 0 ? s[0] + kl_coef * s[1] : s[0]);
         loss[1] = static_cast<float>(s[0]);
         loss[2] = static_cast<float>(s[1]);
         loss[3] = static_cast<float>(s[2]);

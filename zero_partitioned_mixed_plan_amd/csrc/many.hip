@@ -1,5 +1,17 @@
 // Kernels of the many-tensor AdamW step: gradient norm, prologue, update with
 // moments in fp32 or 8 bits, and the moments read back.
+//
+// All of them stream: bf16 gradients, fp32 master weights and bf16 copies
+// move 28 bytes an element with fp32 moments, 16 with 8-bit ones (and a byte
+// per moment and block of 256), the norm 2, the read-back 10.  On 436M
+// elements (two layers of width 4096):
+//   norm          138 us   6.3 TB/s
+//   update, fp32  1.88 ms  6.5 TB/s
+//   update, 8 bit 1.14 ms  6.1 TB/s (62 vector instructions an element, 60%
+//                          of what the units can issue in that time)
+//   read-back     0.70 ms  6.2 TB/s
+// A workgroup finds its tensor through a table of chunks, two dependent
+// scalar loads; one entry serves 512 (fp32) or 2048 (8 bits) elements.
 #include <type_traits>
 
 #include "device.h"
