@@ -672,9 +672,8 @@ void zero_many_destroy(zero_many_t* many); /* NULL is a no-op */
  * moments may be NULL as a whole when only zero_many_grad_norm is called;
  * param may be NULL (no half copy).  exp_avg and exp_avg_sq point to floats
  * (32 bits) or code bytes; the scale arrays, one byte per block, are for 8
- * bits only.  Pointers are aligned to their element; 16-byte aligned
- * fp32 and gradients, 8-byte aligned half gradients and parameters and
- * 4-byte aligned codes take the wide path. */
+ * bits only.  Pointers are aligned to their element; 128-byte aligned ones
+ * are fastest, and tensors packed end to end cost up to a tenth more. */
 typedef struct {
     const void* const* grad;
     float* const* master;

@@ -181,6 +181,22 @@ def test_steps(bits, gdt, pdt, shift):
     assert torch.equal(one, vals[1])
 
 
+@pytest.mark.parametrize("bits", [8, 32])
+@pytest.mark.parametrize("shift", [5, 31, 33])
+def test_steps_at_odd_addresses(bits, shift):
+    """Tensors that start anywhere in a cache line, sizes about its and a chunk's end."""
+    sizes = [1, 31, 32, 33, 480, 481, 482, 511, 512, 513, 991, 2047, 2048, 2049, 4097]
+    m = Model(sizes, "bf16", "bf16", bits, shift, seed=shift)
+    z.zero_many_state_upload(m.many, 0, z.LossScaler(1.0, dynamic=False), seed=8)
+    for t in range(1, 4):
+        m.new_grads()
+        sumsq, flag, want = _norm(m)
+        assert abs(sumsq.item() - want) <= sum(sizes) * 2.0 ** -53 * want and flag.item() == 0
+        z.zero_many_adam_step(m.many, m.hp, flag=flag)
+        m.plain_step(t, 1.0, 1.0, 8)
+        m.check()
+
+
 def _wide(bits):
     """Moments over forty orders of magnitude, subnormals and huge values."""
     m = Model([3000, 777], "f32", "bf16", bits, seed=4, groups=1)

@@ -878,11 +878,14 @@ def _pointers(tensors, name: str, numels, dtypes, may_be_none: bool = False):
         raise ValueError(f"need {len(numels)} entries in {name}, got {len(tensors)}")
     dtype = None
     ptrs = (ctypes.c_void_p * max(len(tensors), 1))()
-    for i, t in enumerate(tensors):
+    for i, (t, n) in enumerate(zip(tensors, numels)):
         if t is None and may_be_none:
             continue
-        _require(t, f"{name}[{i}]", int(numels[i]), dtypes if dtype is None else (dtype,))
-        dtype = t.dtype
+        # the common case without a call per check: models have thousands of tensors
+        if not (dtype is not None and t.dtype is dtype and t.is_cuda and t.is_contiguous() and
+                t.numel() >= n):
+            _require(t, f"{name}[{i}]", n, dtypes if dtype is None else (dtype,))
+            dtype = t.dtype
         ptrs[i] = t.data_ptr()
     return ptrs, dtype
 

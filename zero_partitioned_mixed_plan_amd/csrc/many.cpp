@@ -11,11 +11,6 @@ using namespace zmi;
 
 namespace {
 
-int64_t chunks_of(const zero_many* w, int64_t numel) {
-    const int64_t chunk = many_chunk(w->bits);
-    return (numel + chunk - 1) / chunk;
-}
-
 size_t up256(size_t n) { return (n + 255) / 256 * 256; }
 
 // Sections of the device allocation.
@@ -54,7 +49,7 @@ int ensure(zero_many* w, hipStream_t s) {
     std::vector<uint32_t> chunks;
     chunks.reserve(static_cast<size_t>(w->n_chunks));
     for (size_t i = 0; i < w->numels.size(); ++i) {
-        const int64_t n = chunks_of(w, w->numels[i]);
+        const int64_t n = many_chunks(w->numels[i], w->bits);
         chunks.insert(chunks.end(), static_cast<size_t>(n), static_cast<uint32_t>(i));
     }
     void *d = nullptr, *h = nullptr;
@@ -97,12 +92,12 @@ int fill_tensor(const zero_many* w, const zero_many_buffers_t* b, size_t i, int6
     *t = ManyTensor{};
     t->numel = w->numels[i];
     t->chunk0 = chunk0;
+    t->chunks = many_chunks(t->numel, w->bits);
     t->elem0 = w->offsets[i];
     t->group = w->groups[i];
     if (!any) return ZERO_OK;
     t->grad = address(b->grad[i]);
     const uint64_t gsize = b->grad_dtype == ZERO_F32 ? 4 : 2;
-    uint64_t mis = t->grad % (4 * gsize);
     bool off = t->grad % gsize != 0;
     if (full) {
         t->master = address(b->master[i]);
@@ -112,7 +107,6 @@ int fill_tensor(const zero_many* w, const zero_many_buffers_t* b, size_t i, int6
             return fail(ZERO_ENULL, "tensor " + std::to_string(i) +
                                         ": master, exp_avg and exp_avg_sq must be non-NULL");
         }
-        mis |= t->master % 16;
         off |= t->master % 4 != 0;
         if (w->bits == 8) {
             t->m_scale = address(b->exp_avg_scale[i]);
@@ -121,9 +115,7 @@ int fill_tensor(const zero_many* w, const zero_many_buffers_t* b, size_t i, int6
                 return fail(ZERO_ENULL, "tensor " + std::to_string(i) +
                                             ": 8-bit moments need their scales");
             }
-            mis |= t->m % 4 | t->v % 4;
         } else {
-            mis |= t->m % 16 | t->v % 16;
             off |= t->m % 4 != 0 || t->v % 4 != 0;
         }
         if (b->param != nullptr) {
@@ -131,7 +123,6 @@ int fill_tensor(const zero_many* w, const zero_many_buffers_t* b, size_t i, int6
             if (t->param == 0) {
                 return fail(ZERO_ENULL, "tensor " + std::to_string(i) + ": param is NULL");
             }
-            mis |= t->param % 8;
             off |= t->param % 2 != 0;
         }
     }
@@ -139,7 +130,6 @@ int fill_tensor(const zero_many* w, const zero_many_buffers_t* b, size_t i, int6
         return fail(ZERO_EALIGN, "tensor " + std::to_string(i) +
                                      ": a pointer is not aligned to its element");
     }
-    t->wide = mis == 0;
     return ZERO_OK;
 }
 
@@ -192,7 +182,7 @@ int zero_many_create(const int64_t* numels, const int32_t* groups, int32_t n_ten
             w->offsets.push_back(w->padded);
             w->total += n;
             w->padded += (n + kManyBlock - 1) / kManyBlock * kManyBlock;
-            w->n_chunks += chunks_of(w.get(), n);
+            w->n_chunks += many_chunks(n, w->bits);
         }
         *out = w.release();
     } catch (const std::bad_alloc&) {
@@ -254,7 +244,7 @@ int zero_many_bind(zero_many_t* w, const zero_many_buffers_t* b, void* stream) {
         for (size_t i = 0; i < table.size(); ++i) {
             const int rc = fill_tensor(w, b, i, chunk, &table[i]);
             if (rc != ZERO_OK) return rc;
-            chunk += chunks_of(w, w->numels[i]);
+            chunk += many_chunks(w->numels[i], w->bits);
         }
         if (capturing(s)) return fail(ZERO_ESTATE, "zero_many_bind cannot be captured");
         const int rc = ensure(w, s);

@@ -16,6 +16,15 @@ constexpr int kManyPer32 = 2;  // 32 bits: elements of one thread
 constexpr int many_chunk(int bits) {
     return bits == 8 ? kManyWaves * kManyBlocks * kManyBlock : kManyWaves * 64 * kManyPer32;
 }
+// fp32 elements of a cache line, by fewer than which the 32-bit form's chunks
+// may begin before their tensor.
+constexpr int kManyShift = 32;
+// Chunks of a tensor, wherever its elements lie.
+constexpr int64_t many_chunks(int64_t numel, int bits) {
+    return numel <= 0 ? 0
+                      : (numel + (bits == 8 ? 0 : kManyShift - 1) + many_chunk(bits) - 1) /
+                            many_chunk(bits);
+}
 
 // One tensor, as the kernels read it.
 struct ManyTensor {
@@ -26,9 +35,10 @@ struct ManyTensor {
     uint64_t param;  // 0: no half copy
     int64_t numel;
     int64_t chunk0;  // its first chunk
+    int64_t chunks;
     int64_t elem0;   // its first element in the padded order
     int32_t group;
-    int32_t wide;    // every array allows the wide path
+    int32_t _pad;
 };
 
 struct ManyScalars {
