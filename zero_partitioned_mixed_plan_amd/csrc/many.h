@@ -8,8 +8,8 @@
 namespace zmi {
 
 constexpr int kManyBlock = ZERO_MANY_BLOCK;   // elements of one 8-bit scale
-// Elements of one workgroup of the update (a chunk; chunks start at a
-// tensor's start).  8 bits: kManyWaves waves of kManyBlocks blocks each.
+// Elements of one workgroup of the update (a chunk; a tensor's chunks are its
+// own).  8 bits: kManyWaves waves of kManyBlocks blocks each.
 constexpr int kManyBlocks = 2;
 constexpr int kManyWaves = 4;
 constexpr int kManyPer32 = 2;  // 32 bits: elements of one thread
