@@ -688,8 +688,11 @@ typedef struct {
 
 /* Hands the tensors to the handle (again after any of them moved); waits
  * for `stream`, and cannot be captured.  Nothing of the handle may be in
- * flight on another stream, and a captured graph sees the new tensors.  Errors: ZERO_ENULL, ZERO_EINVAL,
- * ZERO_EALIGN, ZERO_ESTATE (capturing, or another device), ZERO_EHIP,
+ * flight on another stream.  A graph captured from the handle sees the new
+ * tensors; what it was captured with stays: the gradients' type, and for a
+ * step or a read-back the moments and the half copies and their type.
+ * Errors: ZERO_ENULL, ZERO_EINVAL, ZERO_EALIGN, ZERO_ESTATE (capturing,
+ * another device, or other types than a captured graph's), ZERO_EHIP,
  * ZERO_ENOMEM. */
 int zero_many_bind(zero_many_t* many, const zero_many_buffers_t* buffers, void* stream);
 

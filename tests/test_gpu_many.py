@@ -404,6 +404,59 @@ def test_graph_replays(bits):
     assert sa == sb and (sa.applied_steps, sa.skipped_steps) == (5, 1)
 
 
+@pytest.mark.parametrize("bits", [8, 32])
+def test_bind_keeps_what_a_graph_was_captured_with(bits):
+    sizes = [300, 5000]
+    m = Model(sizes, "bf16", "bf16", bits, seed=41)
+    z.zero_many_state_upload(m.many, 0, z.LossScaler(1.0, dynamic=False), seed=3)
+    sumsq = torch.zeros(1, dtype=torch.float64, device=DEV)
+    flag = torch.zeros(1, dtype=torch.int32, device=DEV)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=s):
+        z.zero_many_grad_norm(m.many, sumsq, flag)
+        z.zero_many_adam_step(m.many, m.hp, flag=flag, sumsq=sumsq)
+    args = [m.d_g, m.d_p, m.d_m, m.d_v, m.d_ms, m.d_vs, m.d_half]
+    for change in ({0: [g.half() for g in m.d_g]}, {0: [g.float() for g in m.d_g]}, {6: None},
+                   {6: [h.half() for h in m.d_half]}, {k: None for k in range(1, 7)}):
+        with pytest.raises(z.ZeroError, match="captured"):
+            z.zero_many_bind(m.many, *[change.get(i, a) for i, a in enumerate(args)])
+    # tensors without a gradient have no type, and moved ones are seen
+    z.zero_many_bind(m.many, [None, None], *args[1:])
+    graph.replay()
+    torch.cuda.synchronize()
+    assert (sumsq.item(), flag.item()) == (0, 0)
+    m.d_g = [g.clone() for g in m.d_g]
+    m.bind()
+    for t in range(2, 5):
+        m.new_grads()
+        graph.replay()
+        torch.cuda.synchronize()
+        m.plain_step(t, 1.0, 1.0, 3)
+        m.check()
+
+
+def test_a_graph_of_the_norm_keeps_the_gradients_type_alone():
+    g = [torch.ones(1000, device=DEV).bfloat16()]
+    many = z.zero_many_create([1000], state_bits=32)
+    z.zero_many_bind(many, g)
+    sumsq = torch.zeros(1, dtype=torch.float64, device=DEV)
+    flag = torch.zeros(1, dtype=torch.int32, device=DEV)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=s):
+        z.zero_many_grad_norm(many, sumsq, flag)
+    with pytest.raises(z.ZeroError, match="captured"):
+        z.zero_many_bind(many, [g[0].float()])
+    state = [[torch.zeros(1000, device=DEV)] for _ in range(3)]
+    z.zero_many_bind(many, [2 * g[0]], *state)
+    graph.replay()
+    torch.cuda.synchronize()
+    assert (sumsq.item(), flag.item()) == (4000, 0)
+
+
 def test_offsets_past_32_bits():
     """The end of a tensor of more than 2^32 elements, moments in 8 bits."""
     n = (1 << 32) + 1300

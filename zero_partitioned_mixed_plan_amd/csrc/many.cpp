@@ -237,16 +237,27 @@ int zero_many_bind(zero_many_t* w, const zero_many_buffers_t* b, void* stream) {
         return fail(ZERO_EINVAL, "param_dtype must be ZERO_F16 or ZERO_BF16");
     }
     hipStream_t s = static_cast<hipStream_t>(stream);
+    int32_t grad_dtype = b->grad_dtype;
+    const int32_t param_dtype = b->param != nullptr ? b->param_dtype : 0;
     try {
         // every pointer is checked before anything of the handle changes
         std::vector<ManyTensor> table(w->numels.size());
         int64_t chunk = 0;
+        bool grads = false;
         for (size_t i = 0; i < table.size(); ++i) {
             const int rc = fill_tensor(w, b, i, chunk, &table[i]);
             if (rc != ZERO_OK) return rc;
             chunk += many_chunks(w->numels[i], w->bits);
+            grads |= table[i].grad != 0;
         }
         if (capturing(s)) return fail(ZERO_ESTATE, "zero_many_bind cannot be captured");
+        // A captured kernel reads this table through the types it was
+        // captured with: other ones would take it out of the tensors.
+        if (w->captured && !grads) grad_dtype = w->grad_dtype;
+        if ((w->captured && grad_dtype != w->grad_dtype) ||
+            (w->captured_full && (!full || param_dtype != w->param_dtype))) {
+            return fail(ZERO_ESTATE, "a graph captured from this handle holds other types");
+        }
         const int rc = ensure(w, s);
         if (rc != ZERO_OK) return rc;
         hipError_t e = hipStreamSynchronize(s);  // the mirror and the table are free again
@@ -262,8 +273,8 @@ int zero_many_bind(zero_many_t* w, const zero_many_buffers_t* b, void* stream) {
     } catch (const std::bad_alloc&) {
         return fail(ZERO_ENOMEM, "out of host memory");
     }
-    w->grad_dtype = b->grad_dtype;
-    w->param_dtype = b->param != nullptr ? b->param_dtype : 0;
+    w->grad_dtype = grad_dtype;
+    w->param_dtype = param_dtype;
     w->bound = true;
     w->full = full;
     return ZERO_OK;
@@ -347,8 +358,9 @@ int zero_many_grad_norm(zero_many_t* w, double* sumsq, int32_t* flag, void* stre
     }
     const int rc = require_bound(w, false);
     if (rc != ZERO_OK) return rc;
-    const hipError_t e = launch_many_norm(w->view, w->grad_dtype, sumsq, flag,
-                                          static_cast<hipStream_t>(stream));
+    hipStream_t s = static_cast<hipStream_t>(stream);
+    if (!w->captured && capturing(s)) w->captured = true;
+    const hipError_t e = launch_many_norm(w->view, w->grad_dtype, sumsq, flag, s);
     return e == hipSuccess ? ZERO_OK : hip_fail(e, "gradient norm launch");
 }
 
@@ -375,6 +387,7 @@ int zero_many_adam_step(zero_many_t* w, const zero_adam_hparams_t* hp, int32_t n
     if (rc != ZERO_OK) return rc;
     if ((rc = require_state(w)) != ZERO_OK) return rc;
     hipStream_t s = static_cast<hipStream_t>(stream);
+    if (!w->captured_full && capturing(s)) w->captured = w->captured_full = true;
     hipError_t e = launch_many_prologue(w->view, all, n_groups, flag, sumsq, max_norm, norm_out, s);
     if (e != hipSuccess) return hip_fail(e, "step prologue launch");
     e = launch_many_adam(w->view, w->grad_dtype, w->param_dtype, w->bits, s);
@@ -388,8 +401,9 @@ int zero_many_state_values(zero_many_t* w, float* exp_avg, float* exp_avg_sq, vo
     }
     const int rc = require_bound(w, true);
     if (rc != ZERO_OK) return rc;
-    const hipError_t e = launch_many_values(w->view, w->bits, exp_avg, exp_avg_sq,
-                                            static_cast<hipStream_t>(stream));
+    hipStream_t s = static_cast<hipStream_t>(stream);
+    if (!w->captured_full && capturing(s)) w->captured_full = true;
+    const hipError_t e = launch_many_values(w->view, w->bits, exp_avg, exp_avg_sq, s);
     return e == hipSuccess ? ZERO_OK : hip_fail(e, "state values launch");
 }
 

@@ -94,6 +94,9 @@ struct zero_many {
     int device = -1;
     bool ready = false, bound = false, full = false, state_ready = false;
     int32_t grad_dtype = 0, param_dtype = 0;
+    // a graph holds a norm or a step (its gradients' type); a step or a
+    // read-back (the moments, and the half copies' type)
+    bool captured = false, captured_full = false;
     char* d_mem = nullptr;  // block, partials, tensors, chunk table
     char* h_mem = nullptr;  // pinned: block and tensors
     zmi::ManyView view{};
