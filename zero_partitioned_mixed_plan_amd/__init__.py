@@ -737,8 +737,8 @@ def zero_token_logp(logits, labels, logp, lse=None, inv_temperature: float = 1.0
     torch = _torch()
     rows, vocab, stride, code = _matrix(logits, "logits")
     check(lib.zero_token_logp(logits.data_ptr(), code, rows, vocab, stride,
-                              _address(labels, "labels", rows, torch.int64), inv_temperature,
-                              _address(logp, "logp", rows, torch.float32),
+                              _address(labels, "labels", rows, torch.int64),
+                              float(inv_temperature), _address(logp, "logp", rows, torch.float32),
                               _address_or_none(lse, "lse", rows, torch.float32),
                               _stream_handle(stream, logits.device)),
           "zero_token_logp")
@@ -752,7 +752,8 @@ def zero_token_logp_grad(logits, labels, lse, dlogp, dlogits, inv_temperature: f
     rows, vocab, stride, code = _matrix(logits, "logits")
     check(lib.zero_token_logp_grad(logits.data_ptr(), code, rows, vocab, stride,
                                    _address(labels, "labels", rows, torch.int64),
-                                   inv_temperature, _address(lse, "lse", rows, torch.float32),
+                                   float(inv_temperature),
+                                   _address(lse, "lse", rows, torch.float32),
                                    _address(dlogp, "dlogp", rows, torch.float32),
                                    *_dlogits(dlogits, logits),
                                    _stream_handle(stream, logits.device)),
@@ -798,8 +799,8 @@ def zero_preference_loss(logp, ref_logp, seq_offsets, loss, pair_loss, rewards, 
                              float(label_smoothing), _PREFERENCE_KINDS[kind], 1 if average else 0)
     check(lib.zero_preference_loss(logp_ptr, _address_or_none(ref_logp, "ref_logp", rows, f32),
                                    _address_or_none(labels, "labels", rows, torch.int64), rows,
-                                   offsets, pairs, ctypes.byref(cfg), loss_scale, loss_scale_dev,
-                                   _address(loss, "loss", 1, f32),
+                                   offsets, pairs, ctypes.byref(cfg), float(loss_scale),
+                                   loss_scale_dev, _address(loss, "loss", 1, f32),
                                    _address(pair_loss, "pair_loss", pairs, f32),
                                    _address(rewards, "rewards", 2 * pairs, f32),
                                    _address(dlogp, "dlogp", rows, f32),
@@ -827,7 +828,8 @@ def zero_policy_loss(logits, labels, old_logp, advantage, dlogits, logp, terms, 
                                _address_or_none(ref_logp, "ref_logp", rows, f32),
                                _address(advantage, "advantage", rows, f32),
                                _address_or_none(weight, "weight", rows, f32), ctypes.byref(cfg),
-                               loss_scale, loss_scale_dev, _address(logp, "logp", rows, f32),
+                               float(loss_scale), loss_scale_dev,
+                               _address(logp, "logp", rows, f32),
                                _address(terms, "terms", 4 * rows, f32),
                                _address(loss, "loss", 4, f32), *_dlogits(dlogits, logits),
                                _stream_handle(stream, logits.device)), "zero_policy_loss")
